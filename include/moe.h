@@ -499,6 +499,132 @@ MOE_API moe_status moe_balance_global(const double* totals, int64_t m_total, int
                               float alpha, float* f, float* P, float* aux, float* vio, float* bias_inout, float gamma,
                               moe_stream_t stream);
 
+/*
+ * Router projection with a low-rank adapter per request: the logits of a batch whose
+ * tokens belong to many requests, each with an adapter of its own beside the shared W_r.
+ * Passage: "Switch Transformers paper review" (tildalice.io/?p=118), Switch Routing
+ * Step 1 (h = x W_r) and selective precision (the projection in fp32); the adapter is
+ * the low-rank update W_r + s B A of a tuned model, applied per token.
+ *
+ *  With a = adapter_idx[i]:  hidden_i = A_a x_i,  logits_i = x_i W_r + scale_a B_a hidden_i
+ *  (a = -1: no adapter, hidden_i = 0). moe_router_topk takes the result as logits_in.
+ *  x           [m, d] activations, dtype x_dtype (bf16 or fp32).
+ *  w_r         [d, n] fp32 router weight.
+ *  a, b        [n_adapters, r, d] and [n_adapters, n, r], dtype x_dtype (the layouts of two
+ *              linear layers' weights); scale [n_adapters] fp32.
+ *  adapter_idx [m] int32 in any order, -1 .. n_adapters - 1. Any other value counts as -1
+ *              and sets the device error word.
+ *  logits      [m, n] fp32 out. hidden [m, r] fp32 out (for the backward), or NULL.
+ *  Limits: m <= 2^24; 1 <= r <= 64; 1 <= n_adapters <= 1024; d a multiple of 8 (bf16) or
+ *  4 (fp32), at most 2^20. Arrays 16-byte aligned. All sums fp32-accurate: with bf16 x, W_r
+ *  enters the tensor cores as three bf16 parts whose sum is its fp32 value.
+ *  Workspace: moe_router_adapters_workspace_size bytes, any contents; one per call in flight.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE.
+ */
+MOE_API size_t moe_router_adapters_workspace_size(int64_t m, int32_t d, int32_t n, int32_t r, int32_t n_adapters,
+                                                  moe_dtype x_dtype);
+MOE_API moe_status moe_router_adapters(const void* x, moe_dtype x_dtype, const float* w_r, const void* a,
+                                       const void* b, const int32_t* adapter_idx, const float* scale, int64_t m,
+                                       int32_t d, int32_t n, int32_t r, int32_t n_adapters, float* logits,
+                                       float* hidden, void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Backward of moe_router_adapters, from dlogits [m, n] fp32 (moe_router_loss_grad's output):
+ *   du_i = scale_a B_a^T dlogits_i,         dx_i = W_r dlogits_i + A_a^T du_i,
+ *   da_a = sum over its rows of du_i x_i^T,  db_a = scale_a sum of dlogits_i hidden_i^T,
+ *   dw_r = sum_i x_i dlogits_i^T.
+ * Passage: as moe_router_adapters.
+ *  hidden  [m, r] fp32: the forward's output for the same x, a and adapter_idx.
+ *  dx      [m, d] out, dtype x_dtype, rounded once from fp32 sums; NULL: not wanted. Not x itself.
+ *  da, db  [n_adapters, r, d] and [n_adapters, n, r] fp32 out (overwritten; zero for an
+ *          adapter without rows). dw_r [d, n] fp32 out, or NULL (shared projection frozen).
+ *  The other arguments, limits and alignment are moe_router_adapters'. Sums run in a fixed
+ *  order without atomics: the same call gives the same bits.
+ */
+MOE_API size_t moe_router_adapters_grad_workspace_size(int64_t m, int32_t d, int32_t n, int32_t r,
+                                                       int32_t n_adapters, moe_dtype x_dtype);
+MOE_API moe_status moe_router_adapters_grad(const float* dlogits, const void* x, moe_dtype x_dtype, const float* w_r,
+                                            const void* a, const void* b, const int32_t* adapter_idx,
+                                            const float* scale, const float* hidden, int64_t m, int32_t d, int32_t n,
+                                            int32_t r, int32_t n_adapters, void* dx, float* da, float* db,
+                                            float* dw_r, void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Losses of the router over a ragged batch, with per-expert counts.
+ * Passage: "Switch Transformers paper review" (tildalice.io/?p=118), auxiliary load
+ * balancing loss L = alpha N sum_i f_i P_i; "Qwen global-batch load balance"
+ * (agentlenshq.com): the same loss on parts of the batch, averaged. Here the parts are the
+ * batch's sequences, whose lengths differ. (moe_balance_stats is the form for equal
+ * segments in which every token counts.)
+ *
+ *  logits      [m, n] fp32 router logits h (finite or -inf; a row that is -inf throughout
+ *              has no scores: its picks are counted, its scores and z-term are 0).
+ *              Scores p = softmax(h), or 1 / (1 + exp(-h)) for MOE_SIGMOID.
+ *  topk_idx    [m, k] routing decision (distinct experts per token).
+ *  seq_offsets [nseq + 1] int32, ascending: sequence s is rows seq_offsets[s] ..
+ *              seq_offsets[s+1] - 1 (it may be empty). Rows before the first and behind the
+ *              last sequence are padding. Offsets that descend or leave [0, m] set the device
+ *              error word (results are then unspecified).
+ *  token_mask  [m] uint8, 0: the token counts for nothing; NULL: every token counts.
+ *              Padding and masked rows' logits and picks are not read.
+ *  For the T counted tokens of a sequence, or of all of them (row nseq of the tables):
+ *   f_i = count_i / (k T), P_i = mean p_i (both 0 when T = 0).
+ *  loss   [4] out: total, alpha n sum_i f_i P_i over the whole batch, alpha_seq times the mean
+ *         over the sequences with T > 0 of n sum_i f_i P_i, and z_coef times the mean over the
+ *         counted tokens of logsumexp(h)^2.
+ *  counts [nseq + 1, n] int32 out; tokens [nseq + 1] int32 out (T); f, P [nseq + 1, n] fp32 out.
+ *  Sums are fp64 in a fixed order. 1 <= nseq < 2^22. logits 16-byte aligned.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE. A counted token's pick outside [0, n) sets the
+ * device error word and is not counted.
+ */
+MOE_API size_t moe_router_loss_workspace_size(int64_t m, int32_t n, int64_t nseq);
+MOE_API moe_status moe_router_loss(const float* logits, const int32_t* topk_idx, int64_t m, int32_t n, int32_t k,
+                                   const int32_t* seq_offsets, int64_t nseq, const uint8_t* token_mask,
+                                   moe_score_fn fn, float alpha, float alpha_seq, float z_coef, float* loss,
+                                   int32_t* counts, int32_t* tokens, float* f, float* P, void* workspace,
+                                   size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Gradient of the router losses, and of the gates, with respect to the router logits.
+ * Passage: as moe_router_loss (f_i is set by the argmax and held fixed; the gradient flows
+ * through P_i), and Switch Routing Step 3 of "Switch Transformers paper review" (the router
+ * learns through the gate p_i* of y = p_i* E_i*(x)).
+ *  dlogits = dloss * d(total loss)/dh + sum_r dgate_r * d(gate_r)/dh  for a counted token,
+ *  0 for padding and masked rows.
+ *  logits .. z_coef  as in moe_router_loss; counts and tokens are its outputs.
+ *  dloss   [1] fp32 (device), the gradient of the total loss; NULL: 1.
+ *  dgate   [m, k] fp32, the gradient of the gates of topk_idx's picks; NULL: none. Gates as
+ *          moe_router_topk's: p of the pick; with MOE_SOFTMAX, renorm_topk and k >= 2 the
+ *          softmax over the picks' logits.
+ *  dlogits [m, n] fp32 out, 16-byte aligned; not logits itself.
+ * Errors: MOE_ERR_INVALID_ARG.
+ */
+MOE_API moe_status moe_router_loss_grad(const float* logits, const int32_t* topk_idx, int64_t m, int32_t n,
+                                        int32_t k, const int32_t* seq_offsets, int64_t nseq,
+                                        const uint8_t* token_mask, moe_score_fn fn, float alpha, float alpha_seq,
+                                        float z_coef, const int32_t* counts, const int32_t* tokens,
+                                        const float* dloss, const float* dgate, int32_t renorm_topk, float* dlogits,
+                                        moe_stream_t stream);
+
+/*
+ * Backward of moe_combine: the gradient of the expert rows and of the gates.
+ * Passage: "Switch Transformer read for implementation" (molayo1419.me): restore token order,
+ * multiply by the gate; "Switch Transformers paper review", Step 3.
+ *  dgate[i, r] = <dy_i, ybuf[dest_row[i, r]]> (0 for a dropped pick),
+ *  dybuf[dest_row[i, r]] = g_ir dy_i, with the gate that the combine multiplies by (rounded to
+ *  bf16 for dt = MOE_BF16). The residual's gradient is dy.
+ *  dy [m, d], ybuf and dybuf [max_rows, d]: dtype dt, 16-byte aligned, no two of them the same
+ *  buffer. Rows of dybuf that no pick names are left as they were; dybuf NULL: not wanted.
+ *  dest_row [m, k] from moe_capacity_slots: each row is named by one pick at most (a row that
+ *  several picks name would hold one of their products). A row >= max_rows is treated as
+ *  dropped and sets the device error word.
+ *  dgate [m, k] fp32 out, fp32 sums in a fixed order.
+ * Errors: MOE_ERR_INVALID_ARG.
+ */
+MOE_API moe_status moe_combine_grad(const void* dy, const void* ybuf, moe_dtype dt, const int32_t* dest_row,
+                                    const float* topk_gate, int64_t m, int32_t k, int32_t d, int64_t max_rows,
+                                    void* dybuf, float* dgate, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,7 +32,9 @@ EXPORTS = ("moe_last_error", "moe_sync_status", "moe_router_topk_workspace_size"
            "moe_balance_totals", "moe_balance_global", "moe_expert_ffn_combine", "moe_balance_sign_step",
            "moe_expert_ffn_gather", "moe_dispatch_tokens", "moe_router_prepare",
            "moe_balance_step_minibatch", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_combine",
-           "moe_balance_loss_grad")
+           "moe_balance_loss_grad", "moe_router_adapters_workspace_size", "moe_router_adapters",
+           "moe_router_adapters_grad_workspace_size", "moe_router_adapters_grad", "moe_router_loss_workspace_size",
+           "moe_router_loss", "moe_router_loss_grad", "moe_combine_grad")
 
 
 class MoEError(RuntimeError):
@@ -89,6 +91,17 @@ def lib() -> C.CDLL:
         L.moe_balance_totals_workspace_size.restype = SZ
         L.moe_balance_totals.argtypes = [P, P, I64, I32, I32, P, P, SZ, P]
         L.moe_balance_global.argtypes = [P, I64, I32, I32, I32, F, P, P, P, P, P, F, P]
+        for fn in (L.moe_router_adapters_workspace_size, L.moe_router_adapters_grad_workspace_size):
+            fn.argtypes = [I64, I32, I32, I32, I32, I32]
+            fn.restype = SZ
+        L.moe_router_adapters.argtypes = [P, I32, P, P, P, P, P, I64, I32, I32, I32, I32, P, P, P, SZ, P]
+        L.moe_router_adapters_grad.argtypes = [P, P, I32, P, P, P, P, P, P, I64, I32, I32, I32, I32, P, P, P, P, P, SZ,
+                                               P]
+        L.moe_router_loss_workspace_size.argtypes = [I64, I32, I64]
+        L.moe_router_loss_workspace_size.restype = SZ
+        L.moe_router_loss.argtypes = [P, P, I64, I32, I32, P, I64, P, I32, F, F, F, P, P, P, P, P, P, SZ, P]
+        L.moe_router_loss_grad.argtypes = [P, P, I64, I32, I32, P, I64, P, I32, F, F, F, P, P, P, P, I32, P, P]
+        L.moe_combine_grad.argtypes = [P, P, I32, P, P, I64, I32, I32, I64, P, P, P]
         for name in EXPORTS:
             if name not in ("moe_last_error",) and not name.endswith("_workspace_size"):
                 getattr(L, name).restype = C.c_int
@@ -508,3 +521,213 @@ def moe_balance_assign(s, k, beta=None, mode=MOE_QB_SOLVE, rule=MOE_QB_MIDPOINT,
         _ptr(s), m, n, k, _ptr(beta), mode, rule, max_iters, max_repair, _ptr(topk_idx), _ptr(info), _ptr(workspace),
         workspace.numel(), _stream(stream)))
     return topk_idx, beta, info
+
+
+# ---------------------------------------------------------------- training the router, adapters per request
+class _on:
+    """Run a call on the device of its tensors and allocate what it needs on `stream` (so that freed
+    outputs and workspaces are reused in that stream's order)."""
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got {dev}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        self.stack = []
+        if torch.cuda.current_device() != dev.index:
+            self.stack.append(torch.cuda.device(dev))
+        if stream is not None:
+            self.stack.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.stack:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.stack):
+            c.__exit__(*exc)
+
+
+def _need_on(dev, t, dtype, shape, name):
+    """_need, and on `dev`; None is refused."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    _need(t, dtype, shape, name)
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+
+
+def _out(dev, t, dtype, shape, name):
+    """An output: the caller's tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need_on(dev, t, dtype, shape, name)
+    return t
+
+
+def _work_on(dev, workspace, nbytes):
+    """A workspace: the caller's (the library checks its size) or a new one."""
+    if workspace is None:
+        return torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {dev}")
+    return workspace
+
+
+def _torch_dtype_code(dtype) -> int:
+    if dtype == torch.bfloat16:
+        return MOE_BF16
+    if dtype == torch.float32:
+        return MOE_F32
+    raise TypeError(f"unsupported dtype {dtype}")
+
+
+def moe_router_adapters_workspace_size(m, d, n, r, n_adapters, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of moe_router_adapters for activations of `dtype`."""
+    return lib().moe_router_adapters_workspace_size(m, d, n, r, n_adapters, _torch_dtype_code(dtype))
+
+
+def moe_router_adapters_grad_workspace_size(m, d, n, r, n_adapters, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of moe_router_adapters_grad for activations of `dtype`."""
+    return lib().moe_router_adapters_grad_workspace_size(m, d, n, r, n_adapters, _torch_dtype_code(dtype))
+
+
+def moe_router_loss_workspace_size(m, n, nseq) -> int:
+    """Workspace bytes of moe_router_loss."""
+    return lib().moe_router_loss_workspace_size(m, n, nseq)
+
+
+def _adapter_shapes(x, w_r, a, b, adapter_idx, scale):
+    m, d = x.shape
+    n = w_r.shape[1]
+    na, r, _ = a.shape
+    dev = x.device
+    _dtype_code(x)
+    _need_on(dev, x, x.dtype, (m, d), "x")
+    _need_on(dev, w_r, torch.float32, (d, n), "w_r")
+    _need_on(dev, a, x.dtype, (na, r, d), "a")
+    _need_on(dev, b, x.dtype, (na, n, r), "b")
+    _need_on(dev, adapter_idx, torch.int32, (m,), "adapter_idx")
+    _need_on(dev, scale, torch.float32, (na,), "scale")
+    return m, d, n, r, na, dev
+
+
+def moe_router_adapters(x, w_r, a, b, adapter_idx, scale, logits=None, hidden=None, want_hidden=True, workspace=None,
+                        stream=None):
+    """Router logits with a low-rank adapter per token beside the shared projection:
+    logits_i = x_i W_r + scale_a B_a (A_a x_i), a = adapter_idx[i] (-1: none). a [na, r, d] and b [na, n, r] have
+    x's dtype. Returns (logits [m, n] fp32, hidden [m, r] fp32 = A_a x_i, kept for the backward, or None)."""
+    m, d, n, r, na, dev = _adapter_shapes(x, w_r, a, b, adapter_idx, scale)
+    dt = _dtype_code(x)
+    with _on(dev, stream):
+        logits = _out(dev, logits, torch.float32, (m, n), "logits")
+        if hidden is not None or want_hidden:
+            hidden = _out(dev, hidden, torch.float32, (m, r), "hidden")
+        workspace = _work_on(dev, workspace, lib().moe_router_adapters_workspace_size(m, d, n, r, na, dt))
+        _check("moe_router_adapters", lib().moe_router_adapters(
+            _ptr(x), dt, _ptr(w_r), _ptr(a), _ptr(b), _ptr(adapter_idx), _ptr(scale), m, d, n, r, na, _ptr(logits),
+            _ptr(hidden), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return logits, hidden
+
+
+def moe_router_adapters_grad(dlogits, x, w_r, a, b, adapter_idx, scale, hidden, dx=None, da=None, db=None, dw_r=None,
+                             want_dx=True, want_dw_r=False, workspace=None, stream=None):
+    """Backward of moe_router_adapters. Returns (dx [m, d] in x's dtype or None, da [na, r, d] fp32,
+    db [na, n, r] fp32, dw_r [d, n] fp32 or None)."""
+    m, d, n, r, na, dev = _adapter_shapes(x, w_r, a, b, adapter_idx, scale)
+    dt = _dtype_code(x)
+    _need_on(dev, dlogits, torch.float32, (m, n), "dlogits")
+    _need_on(dev, hidden, torch.float32, (m, r), "hidden")
+    with _on(dev, stream):
+        if dx is not None or want_dx:
+            dx = _out(dev, dx, x.dtype, (m, d), "dx")
+        da = _out(dev, da, torch.float32, (na, r, d), "da")
+        db = _out(dev, db, torch.float32, (na, n, r), "db")
+        if dw_r is not None or want_dw_r:
+            dw_r = _out(dev, dw_r, torch.float32, (d, n), "dw_r")
+        workspace = _work_on(dev, workspace, lib().moe_router_adapters_grad_workspace_size(m, d, n, r, na, dt))
+        _check("moe_router_adapters_grad", lib().moe_router_adapters_grad(
+            _ptr(dlogits), _ptr(x), dt, _ptr(w_r), _ptr(a), _ptr(b), _ptr(adapter_idx), _ptr(scale), _ptr(hidden), m,
+            d, n, r, na, _ptr(dx), _ptr(da), _ptr(db), _ptr(dw_r), _ptr(workspace), workspace.numel(),
+            _stream(stream)))
+    return dx, da, db, dw_r
+
+
+def _loss_shapes(logits, topk_idx, seq_offsets, token_mask):
+    m, n = logits.shape
+    k = topk_idx.shape[1]
+    nseq = seq_offsets.shape[0] - 1
+    dev = logits.device
+    _need_on(dev, logits, torch.float32, (m, n), "logits")
+    _need_on(dev, topk_idx, torch.int32, (m, k), "topk_idx")
+    _need_on(dev, seq_offsets, torch.int32, (nseq + 1,), "seq_offsets")
+    if token_mask is not None:
+        _need_on(dev, token_mask, torch.uint8, (m,), "token_mask")
+    return m, n, k, nseq, dev
+
+
+def moe_router_loss(logits, topk_idx, seq_offsets, token_mask=None, score_fn=MOE_SOFTMAX, alpha=1e-2, alpha_seq=0.0,
+                    z_coef=0.0, out=None, workspace=None, stream=None):
+    """Balance loss of the counted tokens of a ragged batch, its sequence-wise mean and the z-loss. Returns
+    dict(loss [4] (total, batch, sequences, z), counts [nseq+1, n] int32, tokens [nseq+1] int32, f, P [nseq+1, n]);
+    row nseq is the whole batch."""
+    m, n, k, nseq, dev = _loss_shapes(logits, topk_idx, seq_offsets, token_mask)
+    with _on(dev, stream):
+        out = dict() if out is None else out
+        res = dict(loss=_out(dev, out.get("loss"), torch.float32, (4,), "loss"),
+                   counts=_out(dev, out.get("counts"), torch.int32, (nseq + 1, n), "counts"),
+                   tokens=_out(dev, out.get("tokens"), torch.int32, (nseq + 1,), "tokens"),
+                   f=_out(dev, out.get("f"), torch.float32, (nseq + 1, n), "f"),
+                   P=_out(dev, out.get("P"), torch.float32, (nseq + 1, n), "P"))
+        workspace = _work_on(dev, workspace, lib().moe_router_loss_workspace_size(m, n, nseq))
+        _check("moe_router_loss", lib().moe_router_loss(
+            _ptr(logits), _ptr(topk_idx), m, n, k, _ptr(seq_offsets), nseq, _ptr(token_mask), score_fn, alpha,
+            alpha_seq, z_coef, _ptr(res["loss"]), _ptr(res["counts"]), _ptr(res["tokens"]), _ptr(res["f"]),
+            _ptr(res["P"]), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return res
+
+
+def moe_router_loss_grad(logits, topk_idx, seq_offsets, counts, tokens, token_mask=None, score_fn=MOE_SOFTMAX,
+                         alpha=1e-2, alpha_seq=0.0, z_coef=0.0, dloss=None, dgate=None, renorm_topk=0, dlogits=None,
+                         stream=None):
+    """Gradient of moe_router_loss's total (times the device scalar dloss [1], 1 without it) and of the gates
+    (dgate [m, k]) with respect to the logits. Returns dlogits [m, n]; padding and masked rows are 0."""
+    m, n, k, nseq, dev = _loss_shapes(logits, topk_idx, seq_offsets, token_mask)
+    _need_on(dev, counts, torch.int32, (nseq + 1, n), "counts")
+    _need_on(dev, tokens, torch.int32, (nseq + 1,), "tokens")
+    if dloss is not None:
+        _need_on(dev, dloss, torch.float32, (1,), "dloss")
+    if dgate is not None:
+        _need_on(dev, dgate, torch.float32, (m, k), "dgate")
+    with _on(dev, stream):
+        dlogits = _out(dev, dlogits, torch.float32, (m, n), "dlogits")
+        _check("moe_router_loss_grad", lib().moe_router_loss_grad(
+            _ptr(logits), _ptr(topk_idx), m, n, k, _ptr(seq_offsets), nseq, _ptr(token_mask), score_fn, alpha,
+            alpha_seq, z_coef, _ptr(counts), _ptr(tokens), _ptr(dloss), _ptr(dgate), renorm_topk, _ptr(dlogits),
+            _stream(stream)))
+    return dlogits
+
+
+def moe_combine_grad(dy, ybuf, dest_row, topk_gate, dybuf=None, dgate=None, want_dybuf=True, stream=None):
+    """Backward of moe_combine: (dybuf [max_rows, d] with dybuf[dest_row[i, r]] = g_ir dy_i or None,
+    dgate [m, k] fp32 = <dy_i, ybuf[dest_row[i, r]]>, 0 for dropped picks). A dybuf made here is zero in the rows
+    that no pick names; a given one keeps them as they were."""
+    m, d = dy.shape
+    k = dest_row.shape[1]
+    max_rows = ybuf.shape[0]
+    dev = dy.device
+    dt = _dtype_code(dy)
+    _need_on(dev, dy, dy.dtype, (m, d), "dy")
+    _need_on(dev, ybuf, dy.dtype, (max_rows, d), "ybuf")
+    _need_on(dev, dest_row, torch.int32, (m, k), "dest_row")
+    _need_on(dev, topk_gate, torch.float32, (m, k), "topk_gate")
+    with _on(dev, stream):
+        if dybuf is None and want_dybuf:
+            dybuf = torch.zeros((max_rows, d), dtype=dy.dtype, device=dev)
+        if dybuf is not None:
+            _need_on(dev, dybuf, dy.dtype, (max_rows, d), "dybuf")
+        dgate = _out(dev, dgate, torch.float32, (m, k), "dgate")
+        _check("moe_combine_grad", lib().moe_combine_grad(
+            _ptr(dy), _ptr(ybuf), dt, _ptr(dest_row), _ptr(topk_gate), m, k, d, max_rows, _ptr(dybuf), _ptr(dgate),
+            _stream(stream)))
+    return dybuf, dgate

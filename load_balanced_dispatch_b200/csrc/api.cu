@@ -62,6 +62,28 @@ int run_balance_step_minibatch(const float* s, int64_t m, int n, int k, float* b
 int run_balance_assign(const float* s, int64_t m, int n, int k, float* beta, int mode, int rule, int max_iters,
                        int max_repair, int32_t* topk_idx, int32_t* info, void* workspace, cudaStream_t stream,
                        const char** err);
+size_t router_adapters_workspace_bytes(int64_t m, int32_t d, int32_t n, int32_t r, int32_t na, moe_dtype dt);
+cudaError_t launch_router_adapters(const void* x, moe_dtype dt, const float* w_r, const void* a, const void* b,
+                                   const int32_t* idx, const float* scale, int64_t m, int d, int n, int r, int na,
+                                   float* logits, float* hidden, void* workspace, cudaStream_t stream);
+size_t router_adapters_grad_workspace_bytes(int64_t m, int32_t d, int32_t n, int32_t r, int32_t na, moe_dtype dt);
+cudaError_t launch_router_adapters_grad(const float* dh, const void* x, moe_dtype dt, const float* w_r, const void* a,
+                                        const void* b, const int32_t* idx, const float* scale, const float* hidden,
+                                        int64_t m, int d, int n, int r, int na, void* dx, float* da, float* db,
+                                        float* dw_r, void* workspace, cudaStream_t stream);
+size_t router_loss_workspace_bytes(int64_t m, int32_t n, int64_t nseq);
+cudaError_t launch_router_loss(const float* logits, const int32_t* idx, int64_t m, int n, int k, const int32_t* off,
+                               int nseq, const uint8_t* mask, int fn, float alpha, float alpha_seq, float z_coef,
+                               float* loss, int32_t* counts, int32_t* tokens, float* f, float* P, void* workspace,
+                               cudaStream_t stream);
+cudaError_t launch_router_loss_grad(const float* logits, const int32_t* idx, int64_t m, int n, int k,
+                                    const int32_t* off, int nseq, const uint8_t* mask, int fn, float alpha,
+                                    float alpha_seq, float z_coef, const int32_t* counts, const int32_t* tokens,
+                                    const float* dloss, const float* dgate, int renorm, float* dlogits,
+                                    cudaStream_t stream);
+cudaError_t launch_combine_grad(const void* dy, const void* ybuf, moe_dtype dt, const int32_t* dest_row,
+                                const float* gate, int64_t m, int k, int d, int64_t max_rows, void* dybuf,
+                                float* dgate, cudaStream_t stream);
 }  // namespace moe
 
 using namespace moe;
@@ -109,6 +131,8 @@ moe_status moe_sync_status(moe_stream_t stream) {
             case kErrTokenIndex: return fail(MOE_ERR_INVALID_ARG, "device: src_token outside [0, m)");
             case kErrPipelineTimeout: return fail(MOE_ERR_INTERNAL, "device: a pipeline wait timed out");
             case kErrRepair: return fail(MOE_ERR_INTERNAL, "device: balanced-assignment repair failed");
+            case kErrAdapterIndex: return fail(MOE_ERR_INVALID_ARG, "device: adapter index outside [-1, n_adapters)");
+            case kErrSeqOffsets: return fail(MOE_ERR_INVALID_ARG, "device: sequence offsets not ascending inside [0, m]");
             case kErrTotals: return fail(MOE_ERR_INVALID_ARG, "device: a routed-count total is not a non-negative integer");
             default: return fail(MOE_ERR_INTERNAL, "device error code %d", code);
         }
@@ -499,6 +523,149 @@ moe_status moe_balance_assign(const float* s, int64_t m, int32_t n, int32_t k, f
     if (st != MOE_OK) return fail((moe_status)st, "moe_balance_assign: %s", err ? err : "failed");
     g_last_error[0] = 0;
     return MOE_OK;
+}
+
+size_t moe_router_adapters_workspace_size(int64_t m, int32_t d, int32_t n, int32_t r, int32_t n_adapters,
+                                          moe_dtype x_dtype) {
+    return router_adapters_workspace_bytes(m, d, n, r, n_adapters, x_dtype);
+}
+
+size_t moe_router_adapters_grad_workspace_size(int64_t m, int32_t d, int32_t n, int32_t r, int32_t n_adapters,
+                                               moe_dtype x_dtype) {
+    return router_adapters_grad_workspace_bytes(m, d, n, r, n_adapters, x_dtype);
+}
+
+}  // extern "C"
+
+// Argument checks that the adapters' forward and backward share.
+static moe_status adapter_args_ok(moe_dtype dt, int64_t m, int32_t d, int32_t n, int32_t r, int32_t na, const void* x,
+                                  const float* w_r, const void* a, const void* b, const int32_t* idx,
+                                  const float* scale) {
+    REQUIRE(dt == MOE_F32 || dt == MOE_BF16, "unknown dtype");
+    REQUIRE(m >= 0 && m <= ((int64_t)1 << 24), "m must be in [0, 2^24]");
+    REQUIRE(n >= 1 && n <= kMaxExperts, "n must be in [1, %d]", kMaxExperts);
+    REQUIRE(r >= 1 && r <= kMaxRank, "r must be in [1, %d]", kMaxRank);
+    REQUIRE(na >= 1 && na <= kMaxAdapters, "n_adapters must be in [1, %d]", kMaxAdapters);
+    REQUIRE(d >= 1 && d <= (1 << 20) && d % (dt == MOE_BF16 ? 8 : 4) == 0, "d must be a multiple of %d, at most 2^20",
+            dt == MOE_BF16 ? 8 : 4);
+    REQUIRE(w_r && a && b && scale, "w_r, a, b and scale are required");
+    REQUIRE(m == 0 || (x && idx), "x and adapter_idx are required");
+    REQUIRE(aligned16(x) && aligned16(w_r) && aligned16(a) && aligned16(b), "x, w_r, a and b must be 16-byte aligned");
+    return MOE_OK;
+}
+
+extern "C" {
+
+moe_status moe_router_adapters(const void* x, moe_dtype x_dtype, const float* w_r, const void* a, const void* b,
+                               const int32_t* adapter_idx, const float* scale, int64_t m, int32_t d, int32_t n,
+                               int32_t r, int32_t n_adapters, float* logits, float* hidden, void* workspace,
+                               size_t ws_bytes, moe_stream_t stream) {
+    const moe_status st = adapter_args_ok(x_dtype, m, d, n, r, n_adapters, x, w_r, a, b, adapter_idx, scale);
+    if (st != MOE_OK) return st;
+    REQUIRE(m == 0 || logits, "logits is required");
+    REQUIRE(aligned16(logits) && aligned16(hidden), "logits and hidden must be 16-byte aligned");
+    const size_t need = router_adapters_workspace_bytes(m, d, n, r, n_adapters, x_dtype);
+    if (ws_bytes < need || (need && (!workspace || !aligned16(workspace))))
+        return fail(MOE_ERR_WORKSPACE, "moe_router_adapters: 16-byte aligned workspace of %zu bytes required", need);
+    return check_launch(launch_router_adapters(x, x_dtype, w_r, a, b, adapter_idx, scale, m, d, n, r, n_adapters,
+                                               logits, hidden, workspace, stream),
+                        "moe_router_adapters");
+}
+
+moe_status moe_router_adapters_grad(const float* dlogits, const void* x, moe_dtype x_dtype, const float* w_r,
+                                    const void* a, const void* b, const int32_t* adapter_idx, const float* scale,
+                                    const float* hidden, int64_t m, int32_t d, int32_t n, int32_t r,
+                                    int32_t n_adapters, void* dx, float* da, float* db, float* dw_r, void* workspace,
+                                    size_t ws_bytes, moe_stream_t stream) {
+    const moe_status st = adapter_args_ok(x_dtype, m, d, n, r, n_adapters, x, w_r, a, b, adapter_idx, scale);
+    if (st != MOE_OK) return st;
+    REQUIRE(m == 0 || (dlogits && hidden), "dlogits and hidden are required");
+    REQUIRE(da && db, "da and db are required");
+    REQUIRE(aligned16(dlogits) && aligned16(hidden) && aligned16(dx) && aligned16(da) && aligned16(db) && aligned16(dw_r),
+            "dlogits, hidden, dx, da, db and dw_r must be 16-byte aligned");
+    REQUIRE(!dx || dx != x, "dx must not alias x");
+    const size_t need = router_adapters_grad_workspace_bytes(m, d, n, r, n_adapters, x_dtype);
+    if (ws_bytes < need || !workspace || !aligned16(workspace))
+        return fail(MOE_ERR_WORKSPACE, "moe_router_adapters_grad: 16-byte aligned workspace of %zu bytes required", need);
+    return check_launch(launch_router_adapters_grad(dlogits, x, x_dtype, w_r, a, b, adapter_idx, scale, hidden, m, d,
+                                                    n, r, n_adapters, dx, da, db, dw_r, workspace, stream),
+                        "moe_router_adapters_grad");
+}
+
+size_t moe_router_loss_workspace_size(int64_t m, int32_t n, int64_t nseq) {
+    return router_loss_workspace_bytes(m, n, nseq);
+}
+
+}  // extern "C"
+
+// Argument checks that the router losses' forward and backward share.
+static moe_status router_loss_args_ok(const float* logits, const int32_t* topk_idx, int64_t m, int32_t n, int32_t k,
+                                      const int32_t* seq_offsets, int64_t nseq, moe_score_fn fn, float alpha,
+                                      float alpha_seq, float z_coef) {
+    REQUIRE(m >= 0, "m must be >= 0");
+    REQUIRE(n >= 1 && n <= kMaxExperts, "n must be in [1, %d]", kMaxExperts);
+    REQUIRE(k >= 1 && k <= n, "k must be in [1, n]");
+    REQUIRE(m * (int64_t)k < ((int64_t)1 << 31), "m * k must be < 2^31");
+    REQUIRE(nseq >= 1 && nseq < ((int64_t)1 << 22), "nseq must be in [1, 2^22)");
+    REQUIRE(fn == MOE_SOFTMAX || fn == MOE_SIGMOID, "unknown score function");
+    REQUIRE(alpha - alpha == 0.f && alpha_seq - alpha_seq == 0.f && z_coef - z_coef == 0.f,
+            "alpha, alpha_seq and z_coef must be finite");
+    REQUIRE(seq_offsets, "seq_offsets is required");
+    REQUIRE(m == 0 || (logits && topk_idx), "logits and topk_idx are required");
+    REQUIRE(aligned16(logits), "logits must be 16-byte aligned");
+    return MOE_OK;
+}
+
+extern "C" {
+
+moe_status moe_router_loss(const float* logits, const int32_t* topk_idx, int64_t m, int32_t n, int32_t k,
+                           const int32_t* seq_offsets, int64_t nseq, const uint8_t* token_mask, moe_score_fn fn,
+                           float alpha, float alpha_seq, float z_coef, float* loss, int32_t* counts, int32_t* tokens,
+                           float* f, float* P, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    const moe_status st =
+        router_loss_args_ok(logits, topk_idx, m, n, k, seq_offsets, nseq, fn, alpha, alpha_seq, z_coef);
+    if (st != MOE_OK) return st;
+    REQUIRE(loss && counts && tokens && f && P, "loss, counts, tokens, f and P are required");
+    const size_t need = router_loss_workspace_bytes(m, n, nseq);
+    if (ws_bytes < need || !workspace || !aligned16(workspace))
+        return fail(MOE_ERR_WORKSPACE, "moe_router_loss: 16-byte aligned workspace of %zu bytes required", need);
+    return check_launch(launch_router_loss(logits, topk_idx, m, n, k, seq_offsets, (int)nseq, token_mask, (int)fn,
+                                           alpha, alpha_seq, z_coef, loss, counts, tokens, f, P, workspace, stream),
+                        "moe_router_loss");
+}
+
+moe_status moe_router_loss_grad(const float* logits, const int32_t* topk_idx, int64_t m, int32_t n, int32_t k,
+                                const int32_t* seq_offsets, int64_t nseq, const uint8_t* token_mask, moe_score_fn fn,
+                                float alpha, float alpha_seq, float z_coef, const int32_t* counts,
+                                const int32_t* tokens, const float* dloss, const float* dgate, int32_t renorm_topk,
+                                float* dlogits, moe_stream_t stream) {
+    const moe_status st =
+        router_loss_args_ok(logits, topk_idx, m, n, k, seq_offsets, nseq, fn, alpha, alpha_seq, z_coef);
+    if (st != MOE_OK) return st;
+    REQUIRE(counts && tokens, "counts and tokens are required");
+    REQUIRE(m == 0 || dlogits, "dlogits is required");
+    REQUIRE(aligned16(dlogits), "dlogits must be 16-byte aligned");
+    REQUIRE(!dlogits || dlogits != logits, "dlogits must not alias logits");
+    return check_launch(launch_router_loss_grad(logits, topk_idx, m, n, k, seq_offsets, (int)nseq, token_mask,
+                                                (int)fn, alpha, alpha_seq, z_coef, counts, tokens, dloss, dgate,
+                                                renorm_topk ? 1 : 0, dlogits, stream),
+                        "moe_router_loss_grad");
+}
+
+moe_status moe_combine_grad(const void* dy, const void* ybuf, moe_dtype dt, const int32_t* dest_row,
+                            const float* topk_gate, int64_t m, int32_t k, int32_t d, int64_t max_rows, void* dybuf,
+                            float* dgate, moe_stream_t stream) {
+    REQUIRE(dt == MOE_F32 || dt == MOE_BF16, "unknown dtype");
+    REQUIRE(m >= 0 && max_rows >= 0 && max_rows < ((int64_t)1 << 31), "bad m or max_rows");
+    REQUIRE(k >= 1 && k <= kMaxExperts && m * (int64_t)k < ((int64_t)1 << 31), "bad k");
+    REQUIRE(d >= 1 && ((int64_t)d * (dt == MOE_BF16 ? 2 : 4)) % 16 == 0, "d must be a multiple of %d",
+            dt == MOE_BF16 ? 8 : 4);
+    REQUIRE(m == 0 || (dy && dest_row && topk_gate && dgate), "dy, dest_row, topk_gate and dgate are required");
+    REQUIRE(m == 0 || max_rows == 0 || ybuf, "ybuf is required");
+    REQUIRE(aligned16(dy) && aligned16(ybuf) && aligned16(dybuf), "dy, ybuf and dybuf must be 16-byte aligned");
+    REQUIRE(!dybuf || (dybuf != ybuf && dybuf != dy), "dybuf must not alias ybuf or dy");
+    return check_launch(launch_combine_grad(dy, ybuf, dt, dest_row, topk_gate, m, k, d, max_rows, dybuf, dgate, stream),
+                        "moe_combine_grad");
 }
 
 }  // extern "C"

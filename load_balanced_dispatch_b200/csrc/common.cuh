@@ -11,6 +11,8 @@ namespace moe {
 
 constexpr int kMaxExperts = 256;
 constexpr int kNumSMs = 148;
+constexpr int kMaxRank = 64;        // rank of a router adapter
+constexpr int kMaxAdapters = 1024;  // router adapters in one call
 
 // Device error word (one per device): kernels record the first condition they
 // detect and skip the offending access; moe_sync_status() reads and clears it.
@@ -22,6 +24,8 @@ enum : int {
     kErrPipelineTimeout = 4,  // a bounded pipeline wait gave up
     kErrRepair = 5,        // balanced-assignment repair found no valid path
     kErrTotals = 6,        // a routed-count total is not a non-negative integer
+    kErrAdapterIndex = 7,  // adapter_idx outside [-1, n_adapters)
+    kErrSeqOffsets = 8,    // sequence offsets not ascending inside [0, m]
 };
 __device__ int g_error = 0;
 
