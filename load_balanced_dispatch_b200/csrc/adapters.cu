@@ -16,6 +16,7 @@ namespace adp {
 constexpr int kThreads = 256;
 constexpr int kPad = 64;        // a group's rows are padded to this many in the grouped order
 constexpr int kSeg = 512;       // rows of one partial sum of the row contractions
+constexpr int kTile = 256;      // rows of a tensor-core row tile
 constexpr int kPlanThreads = 1024;
 }  // namespace adp
 
@@ -26,10 +27,23 @@ struct AdapterPlan {
     int32_t *goff;   // [na + 2] first grouped position of each group
     int32_t *gcnt;   // [na + 1] rows of each group
     int32_t *sseg;   // [na + 2] first segment (kSeg grouped positions) of each group
+    int32_t *tstart; // [na + 2] first row tile (kTile grouped positions) of each group
 };
 
 static int64_t adapter_padded_rows(int64_t m, int na) { return m + (int64_t)adp::kPad * (na + 1); }
 static int64_t adapter_segments(int64_t rows, int groups) { return (rows + adp::kSeg - 1) / adp::kSeg + groups; }
+
+static size_t adapter_plan_layout(int64_t m, int na, AdapterPlan* plan, char* base) {
+    size_t off = 0;
+    auto take = [&](size_t ints) { char* p = base + off; off += (4 * ints + 255) & ~size_t(255); return (int32_t*)p; };
+    int32_t* p;
+    p = take((size_t)adapter_padded_rows(m, na)); if (plan) plan->perm = p;
+    p = take((size_t)na + 2);                     if (plan) plan->goff = p;
+    p = take((size_t)na + 1);                     if (plan) plan->gcnt = p;
+    p = take((size_t)na + 2);                     if (plan) plan->sseg = p;
+    p = take((size_t)na + 2);                     if (plan) plan->tstart = p;
+    return off;
+}
 
 struct AdapterWs {
     AdapterPlan plan;
@@ -38,14 +52,10 @@ struct AdapterWs {
 };
 
 static size_t adapter_ws_layout(int64_t m, int d, int n, int r, int na, AdapterWs* w, char* base) {
-    size_t off = 0;
+    size_t off = adapter_plan_layout(m, na, w ? &w->plan : nullptr, base);
     auto take = [&](size_t bytes) { char* p = base + off; off += (bytes + 255) & ~size_t(255); return p; };
     char* p;
     const int64_t mp = adapter_padded_rows(m, na);
-    p = take(4 * (size_t)mp);          if (w) w->plan.perm = (int32_t*)p;
-    p = take(4 * (size_t)(na + 2));    if (w) w->plan.goff = (int32_t*)p;
-    p = take(4 * (size_t)(na + 1));    if (w) w->plan.gcnt = (int32_t*)p;
-    p = take(4 * (size_t)(na + 2));    if (w) w->plan.sseg = (int32_t*)p;
     p = take(4 * (size_t)m * r);       if (w) w->du = (float*)p;
     const size_t by_group = (size_t)adapter_segments(mp, na + 1) * r * (size_t)(d > n ? d : n);
     const size_t all = (size_t)adapter_segments(m, 1) * d * n;
@@ -53,16 +63,39 @@ static size_t adapter_ws_layout(int64_t m, int d, int n, int r, int na, AdapterW
     return off;
 }
 
-// Stable grouping of the rows by adapter in one CTA. Warp w takes a run of consecutive rows; a
+// Stable grouping of the rows by adapter in one CTA (block 0). Warp w takes a run of consecutive rows; a
 // histogram per warp, their scan over (group, warp), then each warp places its rows: within 32 rows
-// the lanes of one group rank themselves by a match.
+// the lanes of one group rank themselves by a match. Block 0 also clears the tickets.
+// The other blocks, where the tensor cores need it, write W_r [d, n] fp32 as wsplit [3, n, d] bf16 with
+// W_r = wsplit[0] + wsplit[1] + wsplit[2] (32 x 32 tiles, through shared memory).
 __global__ void __launch_bounds__(adp::kPlanThreads)
-adapter_plan_kernel(const int32_t* __restrict__ idx, int64_t m, int na, AdapterPlan p) {
+adapter_prep_kernel(const int32_t* __restrict__ idx, int64_t m, int na, AdapterPlan p, int32_t* __restrict__ tickets,
+                    int64_t ntickets, const float* __restrict__ w_r, int d, int n,
+                    __nv_bfloat16* __restrict__ wsplit) {
     using namespace adp;
     extern __shared__ int hist[];  // [32][na + 1]
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, G = na + 1;
     pdl_trigger();
     pdl_wait();
+    if (blockIdx.x > 0) {
+        __shared__ float tile[32][33];
+        const int nb = (n + 31) / 32, b = (int)blockIdx.x - 1;
+        const int t0 = b / nb * 32, j0 = b % nb * 32;
+        tile[wid][lane] = (t0 + wid < d && j0 + lane < n) ? w_r[(int64_t)(t0 + wid) * n + j0 + lane] : 0.f;
+        __syncthreads();
+        const int j = j0 + wid, t = t0 + lane;
+        if (j >= n || t >= d) return;
+        const float v = tile[lane][wid];
+        const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
+        const float r1 = v - __bfloat162float(p0);
+        const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
+        const int64_t o = (int64_t)j * d + t, plane = (int64_t)n * d;
+        wsplit[o] = p0;
+        wsplit[plane + o] = p1;
+        wsplit[2 * plane + o] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
+        return;
+    }
+    for (int64_t i = tid; i < ntickets; i += kPlanThreads) tickets[i] = 0;
     for (int i = tid; i < 32 * G; i += kPlanThreads) hist[i] = 0;
     __syncthreads();
     const int64_t per = ((m + 31) / 32 + 31) / 32 * 32;  // rows per warp, a multiple of 32
@@ -88,21 +121,23 @@ adapter_plan_kernel(const int32_t* __restrict__ idx, int64_t m, int na, AdapterP
     }
     __syncthreads();
     if (wid == 0) {
-        int base = 0, seg = 0;
+        int base = 0, seg = 0, til = 0;
         for (int g0 = 0; g0 < G; g0 += 32) {
             const int g = g0 + lane;
             const int c = g < G ? p.gcnt[g] : 0;
-            const int pc = (c + kPad - 1) / kPad * kPad, sc = (pc + kSeg - 1) / kSeg;
-            int a = pc, s = sc;
+            const int pc = (c + kPad - 1) / kPad * kPad, sc = (pc + kSeg - 1) / kSeg, tc = (pc + kTile - 1) / kTile;
+            int a = pc, s = sc, t = tc;
             for (int o = 1; o < 32; o <<= 1) {
-                const int ta = __shfl_up_sync(0xffffffffu, a, o), ts = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) { a += ta; s += ts; }
+                const int ua = __shfl_up_sync(0xffffffffu, a, o), us = __shfl_up_sync(0xffffffffu, s, o);
+                const int ut = __shfl_up_sync(0xffffffffu, t, o);
+                if (lane >= o) { a += ua; s += us; t += ut; }
             }
-            if (g < G) { p.goff[g] = base + a - pc; p.sseg[g] = seg + s - sc; }
+            if (g < G) { p.goff[g] = base + a - pc; p.sseg[g] = seg + s - sc; p.tstart[g] = til + t - tc; }
             base += __shfl_sync(0xffffffffu, a, 31);
             seg += __shfl_sync(0xffffffffu, s, 31);
+            til += __shfl_sync(0xffffffffu, t, 31);
         }
-        if (lane == 0) { p.goff[G] = base; p.sseg[G] = seg; }
+        if (lane == 0) { p.goff[G] = base; p.sseg[G] = seg; p.tstart[G] = til; }
     }
     __syncthreads();
     for (int g = tid; g < G; g += kPlanThreads) {
@@ -130,13 +165,17 @@ adapter_plan_kernel(const int32_t* __restrict__ idx, int64_t m, int na, AdapterP
     }
 }
 
-static cudaError_t launch_adapter_plan(const int32_t* idx, int64_t m, int na, const AdapterPlan& p,
+// wsplit == NULL: the plan alone.
+static cudaError_t launch_adapter_prep(const int32_t* idx, int64_t m, int na, const AdapterPlan& p, int32_t* tickets,
+                                       int64_t ntickets, const float* w_r, int d, int n, __nv_bfloat16* wsplit,
                                        cudaStream_t stream) {
     const size_t smem = sizeof(int) * 32 * (size_t)(na + 1);
-    cudaError_t e = cudaFuncSetAttribute(adapter_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(adapter_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)(sizeof(int) * 32 * (kMaxAdapters + 1)));
     if (e != cudaSuccess) return e;
-    return launch_pdl(adapter_plan_kernel, dim3(1), dim3(adp::kPlanThreads), smem, stream, idx, m, na, p);
+    const unsigned blocks = 1 + (wsplit ? (unsigned)((d + 31) / 32) * (unsigned)((n + 31) / 32) : 0);
+    return launch_pdl(adapter_prep_kernel, dim3(blocks), dim3(adp::kPlanThreads), smem, stream, idx, m, na, p, tickets,
+                      ntickets, w_r, d, n, wsplit);
 }
 
 // ---- forward: R rows per CTA, thread (column, row group); 32 input columns at a time through
@@ -420,91 +459,6 @@ static cudaError_t launch_rows_contract(const TX* X, int np, const TY* Y, int nq
     const int64_t per = (int64_t)np * nq;
     return launch_pdl(rows_fold_kernel, dim3((unsigned)((per + adp::kThreads - 1) / adp::kThreads), grouped ? na : 1),
                       dim3(adp::kThreads), 0, stream, part, per, segs, plan, scale, out);
-}
-
-size_t router_adapters_workspace_bytes(int64_t m, int32_t d, int32_t n, int32_t r, int32_t na, moe_dtype dt) {
-    (void)m; (void)d; (void)n; (void)r; (void)na; (void)dt;
-    return 0;
-}
-
-size_t router_adapters_grad_workspace_bytes(int64_t m, int32_t d, int32_t n, int32_t r, int32_t na, moe_dtype dt) {
-    (void)dt;
-    if (m < 0 || d < 1 || n < 1 || r < 1 || na < 1) return 0;
-    return adapter_ws_layout(m, d, n, r, na, nullptr, nullptr);
-}
-
-template <typename T>
-static cudaError_t launch_adapters_rows(const T* x, const float* w_r, const T* a, const T* b, const int32_t* idx,
-                                        const float* scale, int64_t m, int d, int n, int r, int na, float* logits,
-                                        float* hidden, cudaStream_t stream) {
-#define MOE_ADAPTER_ROWS(NP)                                                                                       \
-    do {                                                                                                           \
-        constexpr int RG = adp::kThreads / NP, R = RG > 16 ? RG : 16;                                              \
-        return launch_pdl(adapters_rows_kernel<T, NP>, dim3((unsigned)((m + R - 1) / R)), dim3(adp::kThreads), 0,  \
-                          stream, x, w_r, a, b, idx, scale, m, d, n, r, na, logits, hidden);                       \
-    } while (0)
-    if (n <= 8) MOE_ADAPTER_ROWS(8);
-    if (n <= 16) MOE_ADAPTER_ROWS(16);
-    if (n <= 32) MOE_ADAPTER_ROWS(32);
-    if (n <= 64) MOE_ADAPTER_ROWS(64);
-    if (n <= 128) MOE_ADAPTER_ROWS(128);
-    MOE_ADAPTER_ROWS(256);
-#undef MOE_ADAPTER_ROWS
-}
-
-cudaError_t launch_router_adapters(const void* x, moe_dtype dt, const float* w_r, const void* a, const void* b,
-                                   const int32_t* idx, const float* scale, int64_t m, int d, int n, int r, int na,
-                                   float* logits, float* hidden, void* workspace, cudaStream_t stream) {
-    (void)workspace;
-    if (m == 0) return cudaSuccess;
-    if (dt == MOE_BF16)
-        return launch_adapters_rows(static_cast<const __nv_bfloat16*>(x), w_r, static_cast<const __nv_bfloat16*>(a),
-                                    static_cast<const __nv_bfloat16*>(b), idx, scale, m, d, n, r, na, logits, hidden,
-                                    stream);
-    return launch_adapters_rows(static_cast<const float*>(x), w_r, static_cast<const float*>(a),
-                                static_cast<const float*>(b), idx, scale, m, d, n, r, na, logits, hidden, stream);
-}
-
-template <typename T>
-static cudaError_t launch_adapters_grad_t(const float* dh, const T* x, const float* w_r, const T* a, const T* b,
-                                          const int32_t* idx, const float* scale, const float* hidden, int64_t m,
-                                          int d, int n, int r, int na, T* dx, float* da, float* db, float* dw_r,
-                                          void* workspace, cudaStream_t stream) {
-    AdapterWs w;
-    adapter_ws_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
-    cudaError_t e = launch_adapter_plan(idx, m, na, w.plan, stream);
-    if (e != cudaSuccess) return e;
-    if (m > 0) {
-        const int rows = adp::kThreads / 32;
-        e = launch_pdl(adapters_du_kernel<T>, dim3((unsigned)((m + rows - 1) / rows)), dim3(adp::kThreads), 0, stream,
-                       dh, b, idx, scale, m, n, r, na, w.du);
-        if (e != cudaSuccess) return e;
-        if (dx) {
-            e = launch_pdl(adapters_dx_kernel<T>, dim3((unsigned)((m + 15) / 16), (unsigned)((d + 127) / 128)),
-                           dim3(adp::kThreads), 0, stream, dh, w_r, a, idx, w.du, m, d, n, r, na, dx);
-            if (e != cudaSuccess) return e;
-        }
-    }
-    e = launch_rows_contract(x, d, w.du, r, m, na, w.plan, nullptr, w.part, da, stream);
-    if (e != cudaSuccess) return e;
-    e = launch_rows_contract(hidden, r, dh, n, m, na, w.plan, scale, w.part, db, stream);
-    if (e != cudaSuccess || !dw_r) return e;
-    AdapterPlan none = {};
-    return launch_rows_contract(dh, n, x, d, m, na, none, nullptr, w.part, dw_r, stream);
-}
-
-cudaError_t launch_router_adapters_grad(const float* dh, const void* x, moe_dtype dt, const float* w_r, const void* a,
-                                        const void* b, const int32_t* idx, const float* scale, const float* hidden,
-                                        int64_t m, int d, int n, int r, int na, void* dx, float* da, float* db,
-                                        float* dw_r, void* workspace, cudaStream_t stream) {
-    if (dt == MOE_BF16)
-        return launch_adapters_grad_t(dh, static_cast<const __nv_bfloat16*>(x), w_r,
-                                      static_cast<const __nv_bfloat16*>(a), static_cast<const __nv_bfloat16*>(b), idx,
-                                      scale, hidden, m, d, n, r, na, static_cast<__nv_bfloat16*>(dx), da, db, dw_r,
-                                      workspace, stream);
-    return launch_adapters_grad_t(dh, static_cast<const float*>(x), w_r, static_cast<const float*>(a),
-                                  static_cast<const float*>(b), idx, scale, hidden, m, d, n, r, na,
-                                  static_cast<float*>(dx), da, db, dw_r, workspace, stream);
 }
 
 }  // namespace moe

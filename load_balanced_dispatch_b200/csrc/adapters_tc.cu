@@ -1,0 +1,454 @@
+// adapters_tc.cu -- the router projection with a low-rank adapter per request on the tensor cores
+// (bf16 activations). The operator is described in adapters.cu.
+//
+// Forward. Rows are grouped by adapter (adapters.cu, AdapterPlan), so that the 256 rows of a tile share
+// one A_a; a tile's B operand is [W0; W1; W2; A_a], where W0 + W1 + W2 = W_r in three bf16 parts (every
+// product exact, fp32 accumulation), and x is read once for the projection and the adapter together:
+//   router_adapters_tc_kernel  one persistent CTA per SM, 384 threads:
+//     warp 0      TMA: 64 columns of x (rows that follow one another: 32-row boxes; else four rows a
+//                 gather) and of the B operand per stage
+//     warp 1      tcgen05.mma, M = 128 twice (the two halves of the tile share the B operand)
+//     warps 4-11  drain: a thread owns a row; every kDrain K blocks the accumulators are added into fp32
+//                 registers with round-to-nearest adds (the tensor core's own adds truncate, so a long run
+//                 in TMEM would drift); then the epilogue adds s B_a u and stores logits and u.
+// The K blocks of all tiles form one line that is cut into equal runs, one per CTA, whatever the groups'
+// sizes are. A tile that a cut divides is finished by the last of its CTAs to arrive: each writes its
+// partial sums and takes a ticket, nobody waits, and the sums are added in CTA order (the same bits
+// whoever comes last).
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+namespace atc {
+constexpr int BM = 256, BK = 64, kThreads = 384, kDrain = 4;
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int kMinRun = 4;  // K blocks per CTA at least: shorter runs spend their time on partial sums
+}  // namespace atc
+
+struct AtcShared {
+    uint64_t full[4], empty[4], tfull, tempty;
+    uint32_t tmem_base;
+    int abort_flag;
+    int last;
+};
+
+// The part of a CTA's run that lies in one unit (row tile x column tile).
+struct AtcSegment {
+    int64_t unit;
+    int kb0, kb1;
+};
+
+template <int NP, int RP>
+struct AtcTile {
+    static constexpr bool FUSED = 3 * NP + RP <= 256;
+    static constexpr int ACOLS = FUSED ? 3 * NP + RP : NP + RP;  // accumulator columns of a half tile
+    static constexpr int B_BYTES = (3 * NP + RP) * 128;
+    static constexpr int STAGE = atc::A_BYTES + B_BYTES;
+    static constexpr int STAGES = STAGE <= 65536 ? 3 : 2;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + (size_t)NP * RP * 4 + sizeof(AtcShared);
+    static_assert(2 * ACOLS <= 512, "both halves' accumulators fit the TMEM");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// tile::gather4: four rows of 64 columns (the map's box is one row high)
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int r0, int r1,
+                                            int r2, int r3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+        : "memory");
+}
+
+// Largest g in [0, groups) with start[g] <= t.
+__device__ __forceinline__ int atc_group(const int32_t* __restrict__ start, int groups, int t) {
+    int lo = 0, hi = groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= t) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+template <int NP, int RP>
+__global__ void __launch_bounds__(atc::kThreads, 1)
+router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
+                          const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                          const __nv_bfloat16* __restrict__ bmat, const float* __restrict__ scale, int d, int n, int r,
+                          int na, int nct, AdapterPlan plan, float* __restrict__ part, int32_t* __restrict__ tickets,
+                          float* __restrict__ logits, float* __restrict__ hidden) {
+    using namespace atc;
+    using T = AtcTile<NP, RP>;
+    constexpr int STAGES = T::STAGES, ACOLS = T::ACOLS;
+    constexpr uint32_t TCOLS = 2 * ACOLS <= 256 ? 256 : 512;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* sB = reinterpret_cast<float*>(smem + STAGES * T::STAGE);  // [NP][RP] of B_a
+    AtcShared* sh = reinterpret_cast<AtcShared*>(sB + NP * RP);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nkb = (d + BK - 1) / BK;
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) { ptx::mbar_init(&sh->full[s], 1); ptx::mbar_init(&sh->empty[s], 1); }
+        ptx::mbar_init(&sh->tfull, 1);
+        ptx::mbar_init(&sh->tempty, 256);
+        sh->abort_flag = 0;
+        ptx::fence_barrier_init();
+        ptx::prefetch_tensormap(&map_x);
+        ptx::prefetch_tensormap(&map_g);
+        ptx::prefetch_tensormap(&map_w);
+        ptx::prefetch_tensormap(&map_a);
+    }
+    if (warp == 1) ptx::tmem_alloc(&sh->tmem_base, TCOLS);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    pdl_trigger();
+    pdl_wait();  // the plan and the parts of W_r come from the launch before
+    const uint32_t tmem = sh->tmem_base;
+    volatile int* abort_flag = &sh->abort_flag;
+
+    const int groups = na + 1;
+    const int64_t total = (int64_t)plan.tstart[groups] * nct * nkb;
+    int64_t ctas = total / kMinRun;
+    ctas = ctas < 1 ? 1 : (ctas > gridDim.x ? gridDim.x : ctas);
+    const int64_t c = blockIdx.x;
+    const int64_t lo = c < ctas ? c * total / ctas : total, hi = c < ctas ? (c + 1) * total / ctas : total;
+
+    // unit -> tile and column tile, group, first grouped position, rows
+    auto rows_of = [&](int64_t unit, int& ct, int& g, int& p0) -> int {
+        const int tile = (int)(unit / nct);
+        ct = (int)(unit % nct);
+        g = atc_group(plan.tstart, groups, tile);
+        p0 = plan.goff[g] + BM * (tile - plan.tstart[g]);
+        const int cnt = plan.goff[g] + plan.gcnt[g] - p0;
+        return cnt < BM ? cnt : BM;
+    };
+
+    // 384 x 168 registers at launch = 128 x 72 + 256 x 216: the drain keeps a row's sums in registers
+    if (warp < 4) {
+        ptx::regs_less<72>();
+        if (warp == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t pos = lo; ok && pos < hi;) {
+                const int64_t unit = pos / nkb;
+                const int kb0 = (int)(pos - unit * nkb);
+                const int kb1 = (int)min((int64_t)nkb, kb0 + (hi - pos));
+                int ct, g, p0;
+                const int cnt = rows_of(unit, ct, g, p0);
+                const int first = plan.perm[p0];
+                const bool run = plan.perm[p0 + cnt - 1] - first == cnt - 1;  // rows ascend inside a group
+                const bool ad = g < na;
+                // lane l: boxes of 32 rows (l < 8), or gathers of rows 8 l .. 8 l + 7
+                int rid[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) rid[q] = plan.perm[p0 + min(8 * lane + q, cnt - 1)];
+                const int boxes = run ? (cnt + 31) / 32 : 0;
+                const int quads = run ? 0 : (cnt + 3) / 4;
+                const uint32_t bytes = (uint32_t)(boxes * 4096 + quads * 512 + 3 * NP * 128 + (ad ? RP * 128 : 0));
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag));
+                    if (!ok) break;
+                    uint8_t* st = smem + stage * T::STAGE;
+                    uint8_t* sb = st + A_BYTES;
+                    if (lane == 0) ptx::mbar_expect_tx(&sh->full[stage], bytes);
+                    __syncwarp();
+                    if (lane < boxes) ptx::tma_load_2d(st + lane * 4096, &map_x, &sh->full[stage], kb * BK, first + 32 * lane);
+                    if (2 * lane < quads)
+                        tma_gather4(st + lane * 1024, &map_g, &sh->full[stage], kb * BK, rid[0], rid[1], rid[2], rid[3]);
+                    if (2 * lane + 1 < quads)
+                        tma_gather4(st + lane * 1024 + 512, &map_g, &sh->full[stage], kb * BK, rid[4], rid[5], rid[6], rid[7]);
+                    // B rows: fused [W0 W1 W2 A], else [W0 A W1 W2]
+                    if (lane >= 8 && lane < 11) {
+                        const int p = lane - 8;
+                        const int row = p * NP + (!T::FUSED && p > 0 ? RP : 0);
+                        ptx::tma_load_3d(sb + row * 128, &map_w, &sh->full[stage], kb * BK, ct * NP, p);
+                    }
+                    if (lane == 11 && ad)
+                        ptx::tma_load_3d(sb + (T::FUSED ? 3 * NP : NP) * 128, &map_a, &sh->full[stage], kb * BK, 0, g);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                pos += kb1 - kb0;
+            }
+        } else if (warp == 1) {
+            if (lane == 0) {
+                int stage = 0;
+                uint32_t phase = 0, tphase = 0;
+                bool ok = true;
+                for (int64_t pos = lo; ok && pos < hi;) {
+                    const int64_t unit = pos / nkb;
+                    const int kb0 = (int)(pos - unit * nkb);
+                    const int kb1 = (int)min((int64_t)nkb, kb0 + (hi - pos));
+                    int ct, g, p0;
+                    const int cnt = rows_of(unit, ct, g, p0);
+                    const int halves = cnt > 128 ? 2 : 1, wide = g < na ? RP : 0;
+                    const uint32_t idesc = ptx::idesc_bf16_f32(128, (T::FUSED ? 3 * NP : NP) + wide);
+                    const uint32_t idesc_w = ptx::idesc_bf16_f32(128, NP);
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        const int in = (kb - kb0) % kDrain;
+                        if (in == 0) {
+                            ok = ptx::mbar_wait(&sh->tempty, tphase ^ 1u, abort_flag);
+                            if (!ok) break;
+                        }
+                        ok = ptx::mbar_wait(&sh->full[stage], phase, abort_flag);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint32_t sa = ptx::smem_u32(smem + stage * T::STAGE);
+                        const uint64_t bdesc = ptx::sw128_kmajor_desc(sa + A_BYTES);
+                        for (int h = 0; h < halves; ++h) {
+                            const uint64_t adesc = ptx::sw128_kmajor_desc(sa + h * 16384);
+                            const uint32_t acc = tmem + (uint32_t)(h * ACOLS);
+#pragma unroll
+                            for (int kk = 0; kk < BK / 16; ++kk)
+                                ptx::umma_bf16(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc, (in != 0 || kk != 0) ? 1u : 0u);
+                            if (!T::FUSED) {
+#pragma unroll
+                                for (int p = 1; p < 3; ++p) {
+                                    const uint64_t wdesc = ptx::sw128_kmajor_desc(sa + A_BYTES + (p * NP + RP) * 128);
+#pragma unroll
+                                    for (int kk = 0; kk < BK / 16; ++kk)
+                                        ptx::umma_bf16(acc, adesc + 2 * kk, wdesc + 2 * kk, idesc_w, 1u);
+                                }
+                            }
+                        }
+                        ptx::umma_commit(&sh->empty[stage]);
+                        if (in == kDrain - 1 || kb == kb1 - 1) { ptx::umma_commit(&sh->tfull); tphase ^= 1u; }
+                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    }
+                    pos += kb1 - kb0;
+                }
+            }
+        }
+    } else {
+        ptx::regs_more<216>();
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const int row = half * 128 + quad * 32 + lane;  // of the tile
+        const int et = tid - 128;                       // 0 .. 255
+        const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * ACOLS);
+        uint32_t tphase = 0;
+        bool ok = true;
+        for (int64_t pos = lo; pos < hi;) {
+            const int64_t unit = pos / nkb;
+            const int kb0 = (int)(pos - unit * nkb);
+            const int kb1 = (int)min((int64_t)nkb, kb0 + (hi - pos));
+            int ct, g, p0;
+            const int cnt = rows_of(unit, ct, g, p0);
+            const bool ad = g < na, mine = half * 128 < cnt;
+            float acc[NP], u[RP];
+#pragma unroll
+            for (int j = 0; j < NP; ++j) acc[j] = 0.f;
+#pragma unroll
+            for (int j = 0; j < RP; ++j) u[j] = 0.f;
+            for (int kb = kb0; kb < kb1; kb += kDrain) {
+                // after a give-up every warp still walks its loops: the barriers below count them all
+                if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->tfull, tphase, abort_flag));
+                tphase ^= 1u;
+                if (!ok) continue;
+                ptx::tc_fence_after();
+                if (mine) {
+#pragma unroll
+                    for (int q = 0; q < NP / 16; ++q) {
+                        uint32_t v[T::FUSED ? 3 : 1][16];
+#pragma unroll
+                        for (int p = 0; p < (T::FUSED ? 3 : 1); ++p) ptx::tmem_ld16_issue(trow + (uint32_t)(p * NP + q * 16), v[p]);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float b = __uint_as_float(v[0][j]);
+                            if constexpr (T::FUSED)
+                                b = __fadd_rn(__fadd_rn(__uint_as_float(v[2][j]), __uint_as_float(v[1][j])), b);
+                            acc[q * 16 + j] = __fadd_rn(acc[q * 16 + j], b);
+                        }
+                    }
+                    if (ad) {
+#pragma unroll
+                        for (int q = 0; q < RP / 16; ++q) {
+                            uint32_t v[16];
+                            ptx::tmem_ld16_issue(trow + (uint32_t)((T::FUSED ? 3 * NP : NP) + q * 16), v);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) u[q * 16 + j] = __fadd_rn(u[q * 16 + j], __uint_as_float(v[j]));
+                        }
+                    }
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&sh->tempty);
+            }
+            bool finish = true;
+            if (kb0 != 0 || kb1 != nkb) {
+                // a part of the unit: leave the sums, and finish it if every other part is there already
+                float* mp = part + (2 * c + (kb0 == 0 ? 1 : 0)) * (int64_t)(NP + RP) * BM + row;
+                if (ok && mine) {
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) __stcg(mp + (int64_t)j * BM, acc[j]);
+                    if (ad) {
+#pragma unroll
+                        for (int j = 0; j < RP; ++j) __stcg(mp + (int64_t)(NP + j) * BM, u[j]);
+                    }
+                }
+                __threadfence();
+                ptx::named_barrier(1, 256);
+                const int64_t u0 = unit * nkb;
+                const int64_t cf = ((u0 + 1) * ctas + total - 1) / total - 1, cl = ((u0 + nkb) * ctas + total - 1) / total - 1;
+                if (et == 0) sh->last = atomicAdd(tickets + unit, 1) == (int)(cl - cf);
+                ptx::named_barrier(1, 256);
+                finish = sh->last != 0;
+                if (finish) {
+                    __threadfence();
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) acc[j] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < RP; ++j) u[j] = 0.f;
+                    if (mine) {
+                        for (int64_t cc = cf; cc <= cl; ++cc) {
+                            const int64_t at = cc * total / ctas;  // where the CTA's run begins
+                            const float* op = part + (2 * cc + (at <= u0 ? 1 : 0)) * (int64_t)(NP + RP) * BM + row;
+#pragma unroll
+                            for (int j = 0; j < NP; ++j) acc[j] = __fadd_rn(acc[j], __ldcg(op + (int64_t)j * BM));
+                            if (ad) {
+#pragma unroll
+                                for (int j = 0; j < RP; ++j) u[j] = __fadd_rn(u[j], __ldcg(op + (int64_t)(NP + j) * BM));
+                            }
+                        }
+                    }
+                }
+            }
+            if (finish) {  // the same for all eight warps
+                if (ad) {
+                    ptx::named_barrier(1, 256);  // the tile before is done with sB
+                    for (int i = et; i < NP * RP; i += 256) {
+                        const int e = ct * NP + i / RP, q = i % RP;
+                        sB[i] = (e < n && q < r) ? __bfloat162float(bmat[((int64_t)g * n + e) * r + q]) : 0.f;
+                    }
+                    ptx::named_barrier(1, 256);
+                }
+                if (ok && row < cnt) {
+                    const int64_t out = plan.perm[p0 + row];
+                    if (hidden && ct == 0) {
+                        float* hp = hidden + out * r;
+                        if ((r & 3) == 0) {
+#pragma unroll
+                            for (int j = 0; j < RP; j += 4)
+                                if (j < r) *reinterpret_cast<float4*>(hp + j) = make_float4(u[j], u[j + 1], u[j + 2], u[j + 3]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < RP; ++j)
+                                if (j < r) hp[j] = u[j];
+                        }
+                    }
+                    if (ad) {
+                        const float s = scale[g];
+#pragma unroll
+                        for (int j = 0; j < RP; ++j) u[j] *= s;
+#pragma unroll
+                        for (int e = 0; e < NP; ++e) {
+                            float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+                            for (int q = 0; q < RP; q += 4) {
+                                const float4 b4 = *reinterpret_cast<const float4*>(sB + e * RP + q);
+                                t0 = fmaf(u[q], b4.x, t0);
+                                t1 = fmaf(u[q + 1], b4.y, t1);
+                                t0 = fmaf(u[q + 2], b4.z, t0);
+                                t1 = fmaf(u[q + 3], b4.w, t1);
+                            }
+                            acc[e] += t0 + t1;
+                        }
+                    }
+                    float* lp = logits + out * n + ct * NP;
+                    if ((n & 3) == 0) {
+#pragma unroll
+                        for (int e = 0; e < NP; e += 4)
+                            if (ct * NP + e < n)
+                                *reinterpret_cast<float4*>(lp + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < NP; ++e)
+                            if (ct * NP + e < n) lp[e] = acc[e];
+                    }
+                }
+            }
+            pos += kb1 - kb0;
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, TCOLS);
+    }
+}
+
+// ---- host side
+// Column tile of the logits: all n in one tile where the accumulators fit, else equal tiles.
+static void atc_tile(int n, int r, int& np, int& rp, int& nct) {
+    rp = r <= 32 ? 32 : 64;
+    const int most = rp == 32 ? 128 : 64;
+    nct = (n + most - 1) / most;
+    np = ((n + nct - 1) / nct + 31) / 32 * 32;
+}
+
+struct AtcWs {
+    AdapterPlan plan;
+    __nv_bfloat16* wsplit;  // [3, n, d]
+    float* part;            // [2 kNumSMs][NP + RP][256]
+    int32_t* tickets;       // one per unit
+};
+
+static int64_t atc_tiles(int64_t m, int na) { return m / atc::BM + na + 1; }
+
+static size_t atc_layout(int64_t m, int d, int n, int r, int na, AtcWs* w, char* base) {
+    int np, rp, nct;
+    atc_tile(n, r, np, rp, nct);
+    size_t off = 0;
+    auto take = [&](size_t bytes) { char* p = base + off; off += (bytes + 255) & ~size_t(255); return p; };
+    off = adapter_plan_layout(m, na, w ? &w->plan : nullptr, base);
+    char* p;
+    p = take((size_t)3 * n * d * 2);                                 if (w) w->wsplit = (__nv_bfloat16*)p;
+    p = take((size_t)2 * kNumSMs * (np + rp) * atc::BM * 4);          if (w) w->part = (float*)p;
+    p = take(4 * (size_t)(atc_tiles(m, na) * nct));                   if (w) w->tickets = (int32_t*)p;
+    return off;
+}
+
+template <int NP, int RP>
+static cudaError_t launch_atc(const CUtensorMap& mx, const CUtensorMap& mg, const CUtensorMap& mw,
+                              const CUtensorMap& ma, const __nv_bfloat16* b, const float* scale, int d, int n, int r,
+                              int na, int nct, const AtcWs& w, float* logits, float* hidden, cudaStream_t stream) {
+    constexpr size_t smem = AtcTile<NP, RP>::SMEM;
+    // set on every call: the attribute belongs to the current device
+    const cudaError_t e = cudaFuncSetAttribute(router_adapters_tc_kernel<NP, RP>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(router_adapters_tc_kernel<NP, RP>, dim3(kNumSMs), dim3(atc::kThreads), smem, stream, mx, mg, mw,
+                      ma, b, scale, d, n, r, na, nct, w.plan, w.part, w.tickets, logits, hidden);
+}
+
+static cudaError_t launch_router_adapters_tc(const __nv_bfloat16* x, const float* w_r, const __nv_bfloat16* a,
+                                             const __nv_bfloat16* b, const int32_t* idx, const float* scale, int64_t m,
+                                             int d, int n, int r, int na, float* logits, float* hidden, void* workspace,
+                                             cudaStream_t stream) {
+    int np, rp, nct;
+    atc_tile(n, r, np, rp, nct);
+    AtcWs w;
+    atc_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
+    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, w.tickets, atc_tiles(m, na) * nct, w_r, d, n, w.wsplit, stream);
+    if (e != cudaSuccess) return e;
+    CUtensorMap mx, mg, mw, ma;
+    if (!map_2d(&mx, x, (uint64_t)m, (uint64_t)d, 32) || !map_2d(&mg, x, (uint64_t)m, (uint64_t)d, 1) ||
+        !map_3d(&mw, w.wsplit, 3, (uint64_t)n, (uint64_t)d, (uint32_t)np) ||
+        !map_3d(&ma, a, (uint64_t)na, (uint64_t)r, (uint64_t)d, (uint32_t)rp))
+        return cudaErrorInvalidValue;
+#define MOE_ATC(NP, RP) return launch_atc<NP, RP>(mx, mg, mw, ma, b, scale, d, n, r, na, nct, w, logits, hidden, stream)
+    if (rp == 32) {
+        if (np == 32) MOE_ATC(32, 32);
+        if (np == 64) MOE_ATC(64, 32);
+        if (np == 96) MOE_ATC(96, 32);
+        MOE_ATC(128, 32);
+    }
+    if (np == 32) MOE_ATC(32, 64);
+    MOE_ATC(64, 64);
+#undef MOE_ATC
+}
+
+}  // namespace moe
