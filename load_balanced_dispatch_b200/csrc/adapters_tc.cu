@@ -5,8 +5,8 @@
 // one A_a; a tile's B operand is [W0; W1; W2; A_a], where W0 + W1 + W2 = W_r in three bf16 parts (every
 // product exact, fp32 accumulation), and x is read once for the projection and the adapter together:
 //   router_adapters_tc_kernel  one persistent CTA per SM, 384 threads:
-//     warp 0      TMA: 64 columns of x (rows that follow one another: 32-row boxes; else four rows a
-//                 gather) and of the B operand per stage
+//     warps 0,2,3 TMA, 64 columns a stage: warp 0 the B operand and the 32-row slabs of x whose rows follow
+//                 one another, warps 2 and 3 the other slabs, four rows a gather
 //     warp 1      tcgen05.mma, M = 128 twice (the two halves of the tile share the B operand)
 //     warps 4-11  drain: a thread owns a row; every kDrain K blocks the accumulators are added into fp32
 //                 registers with round-to-nearest adds (the tensor core's own adds truncate, so a long run
@@ -128,7 +128,7 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
     // 384 x 168 registers at launch = 128 x 72 + 256 x 216: the drain keeps a row's sums in registers
     if (warp < 4) {
         ptx::regs_less<72>();
-        if (warp == 0) {
+        if (warp != 1) {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -138,41 +138,47 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                 const int kb1 = (int)min((int64_t)nkb, kb0 + (hi - pos));
                 int ct, g, p0;
                 const int cnt = rows_of(unit, ct, g, p0);
-                const int first = plan.perm[p0];
-                const bool run = plan.perm[p0 + cnt - 1] - first == cnt - 1;  // rows ascend inside a group
                 const bool ad = g < na;
-                // lane l: boxes of 32 rows (l < 8), or gathers of rows 8 l .. 8 l + 7
-                int rid[8];
+                // lane s < 8 looks at slab s, the tile's rows 32 s .. 32 s + 31: one box if they follow one another
+                const int left = cnt - 32 * (lane & 7);
+                const int first = left > 0 ? plan.perm[p0 + 32 * (lane & 7)] : 0;
+                const bool run = left > 0 && plan.perm[p0 + 32 * (lane & 7) + min(left, 32) - 1] - first == min(left, 32) - 1;
+                const uint32_t boxes = __ballot_sync(0xffffffffu, run) & 0xffu;
+                const uint32_t gathers = __ballot_sync(0xffffffffu, left > 0 && !run) & 0xffu;
+                // warps 2 and 3: lane q gathers four rows of slab 4 (warp - 2) + q / 8
+                const int slab = 4 * (warp & 1) + (lane >> 3), quad = 32 * slab + 4 * (lane & 7);
+                const bool gather = warp >= 2 && (gathers >> slab & 1u) && quad < cnt;
+                int rid[4];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) rid[q] = plan.perm[p0 + min(8 * lane + q, cnt - 1)];
-                const int boxes = run ? (cnt + 31) / 32 : 0;
-                const int quads = run ? 0 : (cnt + 3) / 4;
-                const uint32_t bytes = (uint32_t)(boxes * 4096 + quads * 512 + 3 * NP * 128 + (ad ? RP * 128 : 0));
+                for (int q = 0; q < 4; ++q) rid[q] = gather ? plan.perm[p0 + min(quad + q, cnt - 1)] : 0;
+                uint32_t bytes = 3 * NP * 128 + (ad ? RP * 128 : 0) + __popc(boxes) * 4096;
+                for (int q = 0; q < 8; ++q)
+                    if (gathers >> q & 1u) bytes += (min(32, cnt - 32 * q) + 3) / 4 * 512;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag));
                     if (!ok) break;
                     uint8_t* st = smem + stage * T::STAGE;
                     uint8_t* sb = st + A_BYTES;
-                    if (lane == 0) ptx::mbar_expect_tx(&sh->full[stage], bytes);
-                    __syncwarp();
-                    if (lane < boxes) ptx::tma_load_2d(st + lane * 4096, &map_x, &sh->full[stage], kb * BK, first + 32 * lane);
-                    if (2 * lane < quads)
-                        tma_gather4(st + lane * 1024, &map_g, &sh->full[stage], kb * BK, rid[0], rid[1], rid[2], rid[3]);
-                    if (2 * lane + 1 < quads)
-                        tma_gather4(st + lane * 1024 + 512, &map_g, &sh->full[stage], kb * BK, rid[4], rid[5], rid[6], rid[7]);
-                    // B rows: fused [W0 W1 W2 A], else [W0 A W1 W2]
-                    if (lane >= 8 && lane < 11) {
-                        const int p = lane - 8;
-                        const int row = p * NP + (!T::FUSED && p > 0 ? RP : 0);
-                        ptx::tma_load_3d(sb + row * 128, &map_w, &sh->full[stage], kb * BK, ct * NP, p);
+                    uint64_t* bar = &sh->full[stage];
+                    if (warp == 0) {
+                        if (lane == 0) ptx::mbar_expect_tx(bar, bytes);
+                        // B rows: fused [W0 W1 W2 A], else [W0 A W1 W2]
+                        if (lane >= 8 && lane < 11) {
+                            const int p = lane - 8;
+                            const int row = p * NP + (!T::FUSED && p > 0 ? RP : 0);
+                            ptx::tma_load_3d(sb + row * 128, &map_w, bar, kb * BK, ct * NP, p);
+                        }
+                        if (lane == 11 && ad)
+                            ptx::tma_load_3d(sb + (T::FUSED ? 3 * NP : NP) * 128, &map_a, bar, kb * BK, 0, g);
+                        if (lane < 8 && run) ptx::tma_load_2d(st + lane * 4096, &map_x, bar, kb * BK, first);
+                    } else if (gather) {
+                        tma_gather4(st + quad * 128, &map_g, bar, kb * BK, rid[0], rid[1], rid[2], rid[3]);
                     }
-                    if (lane == 11 && ad)
-                        ptx::tma_load_3d(sb + (T::FUSED ? 3 * NP : NP) * 128, &map_a, &sh->full[stage], kb * BK, 0, g);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
                 pos += kb1 - kb0;
             }
-        } else if (warp == 1) {
+        } else {
             if (lane == 0) {
                 int stage = 0;
                 uint32_t phase = 0, tphase = 0;
