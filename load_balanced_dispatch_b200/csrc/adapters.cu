@@ -66,12 +66,13 @@ static size_t adapter_ws_layout(int64_t m, int d, int n, int r, int na, AdapterW
 // Stable grouping of the rows by adapter in one CTA (block 0). Warp w takes a run of consecutive rows; a
 // histogram per warp, their scan over (group, warp), then each warp places its rows: within 32 rows
 // the lanes of one group rank themselves by a match. Block 0 also clears the tickets.
-// The other blocks, where the tensor cores need it, write W_r [d, n] fp32 as wsplit [3, n, d] bf16 with
-// W_r = wsplit[0] + wsplit[1] + wsplit[2] (32 x 32 tiles, through shared memory).
+// The other blocks, where the tensor cores need it, write W_r [d, n] fp32 in bf16 parts that add up to it:
+// three parts as wparts [3, n, d] (transposed, for x W_r), or two as wparts [2, d, nk], nk >= n with zeros
+// behind n (for dh W_r^T).
 __global__ void __launch_bounds__(adp::kPlanThreads)
 adapter_prep_kernel(const int32_t* __restrict__ idx, int64_t m, int na, AdapterPlan p, int32_t* __restrict__ tickets,
-                    int64_t ntickets, const float* __restrict__ w_r, int d, int n,
-                    __nv_bfloat16* __restrict__ wsplit) {
+                    int64_t ntickets, const float* __restrict__ w_r, int d, int n, int nk, int parts,
+                    __nv_bfloat16* __restrict__ wparts) {
     using namespace adp;
     extern __shared__ int hist[];  // [32][na + 1]
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, G = na + 1;
@@ -81,18 +82,24 @@ adapter_prep_kernel(const int32_t* __restrict__ idx, int64_t m, int na, AdapterP
         __shared__ float tile[32][33];
         const int nb = (n + 31) / 32, b = (int)blockIdx.x - 1;
         const int t0 = b / nb * 32, j0 = b % nb * 32;
-        tile[wid][lane] = (t0 + wid < d && j0 + lane < n) ? w_r[(int64_t)(t0 + wid) * n + j0 + lane] : 0.f;
-        __syncthreads();
-        const int j = j0 + wid, t = t0 + lane;
-        if (j >= n || t >= d) return;
-        const float v = tile[lane][wid];
+        float v = (t0 + wid < d && j0 + lane < n) ? w_r[(int64_t)(t0 + wid) * n + j0 + lane] : 0.f;
+        int j = j0 + lane, t = t0 + wid;
+        if (parts == 3) {
+            tile[wid][lane] = v;
+            __syncthreads();
+            j = j0 + wid;
+            t = t0 + lane;
+            v = tile[lane][wid];
+        }
+        if (j >= (parts == 3 ? n : nk) || t >= d) return;
         const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
         const float r1 = v - __bfloat162float(p0);
         const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
-        const int64_t o = (int64_t)j * d + t, plane = (int64_t)n * d;
-        wsplit[o] = p0;
-        wsplit[plane + o] = p1;
-        wsplit[2 * plane + o] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
+        const int64_t o = parts == 3 ? (int64_t)j * d + t : (int64_t)t * nk + j;
+        const int64_t plane = parts == 3 ? (int64_t)n * d : (int64_t)d * nk;
+        wparts[o] = p0;
+        wparts[plane + o] = p1;
+        if (parts == 3) wparts[2 * plane + o] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
         return;
     }
     for (int64_t i = tid; i < ntickets; i += kPlanThreads) tickets[i] = 0;
@@ -165,29 +172,30 @@ adapter_prep_kernel(const int32_t* __restrict__ idx, int64_t m, int na, AdapterP
     }
 }
 
-// wsplit == NULL: the plan alone.
+// wparts == NULL: the plan alone.
 static cudaError_t launch_adapter_prep(const int32_t* idx, int64_t m, int na, const AdapterPlan& p, int32_t* tickets,
-                                       int64_t ntickets, const float* w_r, int d, int n, __nv_bfloat16* wsplit,
-                                       cudaStream_t stream) {
+                                       int64_t ntickets, const float* w_r, int d, int n, int nk, int parts,
+                                       __nv_bfloat16* wparts, cudaStream_t stream) {
     const size_t smem = sizeof(int) * 32 * (size_t)(na + 1);
+    // set on every call: the attribute belongs to the current device
     cudaError_t e = cudaFuncSetAttribute(adapter_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)(sizeof(int) * 32 * (kMaxAdapters + 1)));
     if (e != cudaSuccess) return e;
-    const unsigned blocks = 1 + (wsplit ? (unsigned)((d + 31) / 32) * (unsigned)((n + 31) / 32) : 0);
+    const unsigned blocks = 1 + (wparts ? (unsigned)((d + 31) / 32) * (unsigned)((n + 31) / 32) : 0);
     return launch_pdl(adapter_prep_kernel, dim3(blocks), dim3(adp::kPlanThreads), smem, stream, idx, m, na, p, tickets,
-                      ntickets, w_r, d, n, wsplit);
+                      ntickets, w_r, d, n, nk, parts, wparts);
 }
 
 // ---- forward: R rows per CTA, thread (column, row group); 32 input columns at a time through
 // shared memory. The products of 32 columns are summed first and then added to the row's sum, so the
 // rounding errors grow with the number of blocks, not of columns.
-template <typename T, int NPAD>
+template <int NPAD>
 __global__ void __launch_bounds__(adp::kThreads)
-adapters_rows_kernel(const T* __restrict__ x, const float* __restrict__ w_r, const T* __restrict__ a,
-                     const T* __restrict__ bmat, const int32_t* __restrict__ idx, const float* __restrict__ scale,
+adapters_rows_kernel(const float* __restrict__ x, const float* __restrict__ w_r, const float* __restrict__ a,
+                     const float* __restrict__ bmat, const int32_t* __restrict__ idx, const float* __restrict__ scale,
                      int64_t m, int d, int n, int r, int na, float* __restrict__ logits, float* __restrict__ hidden) {
     using namespace adp;
-    constexpr int KC = 32, RG = kThreads / NPAD, R = RG > 16 ? RG : 16, RPT = R / RG, V = Vec16<T>::N;
+    constexpr int KC = 32, RG = kThreads / NPAD, R = RG > 16 ? RG : 16, RPT = R / RG, V = Vec16<float>::N;
     __shared__ float xs[R][KC + 1];
     __shared__ float ws[KC][NPAD + 1];
     __shared__ float us[R][kMaxRank + 1];
@@ -202,7 +210,7 @@ adapters_rows_kernel(const T* __restrict__ x, const float* __restrict__ w_r, con
     for (int k0 = 0; k0 < d; k0 += KC) {
         for (int i = tid; i < R * KC; i += kThreads) {
             const int rr = i / KC, kk = i % KC;
-            xs[rr][kk] = (row0 + rr < m && k0 + kk < d) ? Elem<T>::load(x + (row0 + rr) * d + k0 + kk) : 0.f;
+            xs[rr][kk] = (row0 + rr < m && k0 + kk < d) ? x[(row0 + rr) * d + k0 + kk] : 0.f;
         }
         for (int i = tid; i < KC * n; i += kThreads) {
             const int kk = i / n, j = i % n;
@@ -239,11 +247,11 @@ adapters_rows_kernel(const T* __restrict__ x, const float* __restrict__ w_r, con
             float s[4] = {0.f, 0.f, 0.f, 0.f};
             for (int c = lane * V; c < d; c += 32 * V) {
                 float xv[V], av[V];
-                Vec16<T>::load(x + row * d + c, xv);
+                Vec16<float>::load(x + row * d + c, xv);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if (j0 + q >= r) continue;
-                    Vec16<T>::load(a + ((int64_t)ad * r + j0 + q) * d + c, av);
+                    Vec16<float>::load(a + ((int64_t)ad * r + j0 + q) * d + c, av);
                     float t = 0.f;
 #pragma unroll
                     for (int i = 0; i < V; ++i) t = fmaf(xv[i], av[i], t);
@@ -270,8 +278,8 @@ adapters_rows_kernel(const T* __restrict__ x, const float* __restrict__ w_r, con
             const int ad = idx[row];
             float t = 0.f;
             if (ad >= 0 && ad < na) {
-                const T* bp = bmat + ((int64_t)ad * n + col) * r;
-                for (int j = 0; j < r; ++j) t = fmaf(us[rr][j], Elem<T>::load(bp + j), t);
+                const float* bp = bmat + ((int64_t)ad * n + col) * r;
+                for (int j = 0; j < r; ++j) t = fmaf(us[rr][j], bp[j], t);
             }
             logits[row * n + col] = acc[q] + t;
         }
@@ -279,9 +287,8 @@ adapters_rows_kernel(const T* __restrict__ x, const float* __restrict__ w_r, con
 }
 
 // ---- du_ij = s_a sum_e dh_ie B_a[e, j]: a warp per row, lanes along j
-template <typename T>
 __global__ void __launch_bounds__(adp::kThreads)
-adapters_du_kernel(const float* __restrict__ dh, const T* __restrict__ bmat, const int32_t* __restrict__ idx,
+adapters_du_kernel(const float* __restrict__ dh, const float* __restrict__ bmat, const int32_t* __restrict__ idx,
                    const float* __restrict__ scale, int64_t m, int n, int r, int na, float* __restrict__ du) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
@@ -293,8 +300,8 @@ adapters_du_kernel(const float* __restrict__ dh, const T* __restrict__ bmat, con
     for (int j = lane; j < r; j += 32) {
         float t = 0.f;
         if (has) {
-            const T* bp = bmat + (int64_t)ad * n * r + j;
-            for (int e = 0; e < n; ++e) t = fmaf(dh[row * n + e], Elem<T>::load(bp + (int64_t)e * r), t);
+            const float* bp = bmat + (int64_t)ad * n * r + j;
+            for (int e = 0; e < n; ++e) t = fmaf(dh[row * n + e], bp[(int64_t)e * r], t);
             t *= scale[ad];
         }
         du[row * r + j] = t;
@@ -302,11 +309,10 @@ adapters_du_kernel(const float* __restrict__ dh, const T* __restrict__ bmat, con
 }
 
 // ---- dx: 16 rows x 128 columns of d per CTA
-template <typename T>
 __global__ void __launch_bounds__(adp::kThreads)
-adapters_dx_kernel(const float* __restrict__ dh, const float* __restrict__ w_r, const T* __restrict__ a,
+adapters_dx_kernel(const float* __restrict__ dh, const float* __restrict__ w_r, const float* __restrict__ a,
                    const int32_t* __restrict__ idx, const float* __restrict__ du, int64_t m, int d, int n, int r,
-                   int na, T* __restrict__ dx) {
+                   int na, float* __restrict__ dx) {
     using namespace adp;
     constexpr int R = 16, DC = 128, EC = 32;
     __shared__ float hs[R][kMaxExperts + 1];
@@ -350,19 +356,18 @@ adapters_dx_kernel(const float* __restrict__ dh, const float* __restrict__ w_r, 
         const int ad = idx[row];
         float t = 0.f;
         if (ad >= 0 && ad < na) {
-            const T* ap = a + (int64_t)ad * r * d + c0 + col;
-            for (int j = 0; j < r; ++j) t = fmaf(us[rg * 8 + q][j], Elem<T>::load(ap + (int64_t)j * d), t);
+            const float* ap = a + (int64_t)ad * r * d + c0 + col;
+            for (int j = 0; j < r; ++j) t = fmaf(us[rg * 8 + q][j], ap[(int64_t)j * d], t);
         }
-        Elem<T>::store(dx + row * d + c0 + col, acc[q] + t);
+        dx[row * d + c0 + col] = acc[q] + t;
     }
 }
 
 // ---- row contractions: part[seg][q][p] = sum over the segment's rows of X[row][p] Y[row][q].
 // 64 x 64 tiles, 4 x 4 per thread, 16 rows at a time (summed first, then added). perm == NULL: the
 // rows in order, one group.
-template <typename TX, typename TY>
 __global__ void __launch_bounds__(adp::kThreads)
-rows_outer_kernel(const TX* __restrict__ X, int np, const TY* __restrict__ Y, int nq, int64_t m, int groups,
+rows_outer_kernel(const float* __restrict__ X, int np, const float* __restrict__ Y, int nq, int64_t m, int groups,
                   AdapterPlan plan, float* __restrict__ part) {
     using namespace adp;
     constexpr int RB = 16;
@@ -395,8 +400,8 @@ rows_outer_kernel(const TX* __restrict__ X, int np, const TY* __restrict__ Y, in
             const int rr = i >> 6, c = i & 63;
             int64_t row = -1;
             if (at + rr < end) row = plan.perm ? plan.perm[at + rr] : at + rr;
-            xs[rr][c] = (row >= 0 && p0 + c < np) ? Elem<TX>::load(X + row * np + p0 + c) : 0.f;
-            ys[rr][c] = (row >= 0 && q0 + c < nq) ? Elem<TY>::load(Y + row * nq + q0 + c) : 0.f;
+            xs[rr][c] = (row >= 0 && p0 + c < np) ? X[row * np + p0 + c] : 0.f;
+            ys[rr][c] = (row >= 0 && q0 + c < nq) ? Y[row * nq + q0 + c] : 0.f;
         }
         __syncthreads();
         float blk[4][4];
@@ -444,8 +449,7 @@ rows_fold_kernel(const float* __restrict__ part, int64_t per, int64_t segs, Adap
     out[g * per + i] = scale ? scale[g] * t : t;
 }
 
-template <typename TX, typename TY>
-static cudaError_t launch_rows_contract(const TX* X, int np, const TY* Y, int nq, int64_t m, int na,
+static cudaError_t launch_rows_contract(const float* X, int np, const float* Y, int nq, int64_t m, int na,
                                         const AdapterPlan& plan, const float* scale, float* part, float* out,
                                         cudaStream_t stream) {
     const bool grouped = plan.perm != nullptr;
@@ -453,7 +457,7 @@ static cudaError_t launch_rows_contract(const TX* X, int np, const TY* Y, int nq
                                  : (m + adp::kSeg - 1) / adp::kSeg;
     cudaError_t e = cudaSuccess;
     if (segs > 0)
-        e = launch_pdl(rows_outer_kernel<TX, TY>, dim3((unsigned)((np + 63) / 64), (unsigned)((nq + 63) / 64), (unsigned)segs),
+        e = launch_pdl(rows_outer_kernel, dim3((unsigned)((np + 63) / 64), (unsigned)((nq + 63) / 64), (unsigned)segs),
                        dim3(adp::kThreads), 0, stream, X, np, Y, nq, m, na + 1, plan, part);
     if (e != cudaSuccess) return e;
     const int64_t per = (int64_t)np * nq;

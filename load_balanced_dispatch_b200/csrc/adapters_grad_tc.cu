@@ -1,0 +1,822 @@
+// adapters_grad_tc.cu -- backward of the router projection with adapters on the tensor cores (bf16
+// activations). The operator is described in adapters.cu; rows are in the grouped order of AdapterPlan.
+//
+//   adapters_split_kernel     per row: du = s B_a^T dh, and dh and du as bf16 parts whose sum is the fp32
+//                             value (three parts for the weight gradients, of which dx uses two); dB on
+//                             the way, each CTA's sums over its run of rows to a slot of its own
+//   adapters_dx_tc_kernel     dx = dh W_r^T + du A_a: the parts of dh and du of a row tile stay in shared
+//                             memory while the parts of W_r and A_a stream past, columns of d at a time
+//   rows_contract_tc_kernel   dA_a = du^T x and dW_r = x^T dh: a contraction over rows, x read once per 64
+//                             columns of the other operand
+//   adapters_fold_kernel      dB from the slots, zeros for adapters without rows
+//
+// dx is rounded to bf16 at the end, so two parts a side and three of their four products (2^-16 of a
+// product is left out) lose nothing against that rounding; one part a side would add errors of the
+// rounding's own size. The weight gradients are fp32, so x (exact in bf16) meets three parts.
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+// K rows in memory order, MN contiguous: boxes of 64 MN columns x K rows under the 128-byte swizzle. The
+// next 64 columns are `lbo` bytes on, the next eight rows 1024.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(lbo >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;  // operand A / B is MN-major
+
+namespace asp {
+constexpr int kThreads = 256, kGrid = 2 * kNumSMs, kRows = adp::kPad;
+}
+
+__device__ __forceinline__ void split3(float v, __nv_bfloat16 (&p)[3]) {
+    p[0] = __float2bfloat16_rn(v);
+    const float r1 = v - __bfloat162float(p[0]);
+    p[1] = __float2bfloat16_rn(r1);
+    p[2] = __float2bfloat16_rn(r1 - __bfloat162float(p[1]));
+}
+
+// CTA c takes the row blocks (kRows grouped positions) c nb / grid .. (c + 1) nb / grid - 1. A group's
+// part of dB in CTA c goes to slot c + g: unique, since each next slot advances the CTA or the group.
+// Thread (te, tj) owns dB[te + 32 a][tj + 8 b].
+template <int NE, int NJ>
+__global__ void __launch_bounds__(asp::kThreads)
+adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hidden,
+                      const __nv_bfloat16* __restrict__ bmat, const float* __restrict__ scale, int n, int r, int na,
+                      AdapterPlan plan, int nk, int planes, int64_t mp, __nv_bfloat16* __restrict__ dhp, int pc, int rp,
+                      __nv_bfloat16* __restrict__ dup, float* __restrict__ slots) {
+    using namespace asp;
+    extern __shared__ float sm[];
+    const int hs = n | 1, us = r | 1;
+    float* sh = sm;                 // [kRows][hs] dh
+    float* su = sh + kRows * hs;    // [kRows][us] u
+    float* sb = su + kRows * us;    // [n][us] B_a
+    __shared__ int rows[kRows];
+    const int tid = threadIdx.x, te = tid >> 3, tj = tid & 7;
+    pdl_trigger();
+    pdl_wait();
+    const int64_t nb = plan.goff[na + 1] / kRows, c = blockIdx.x;
+    const int64_t b0 = c * nb / gridDim.x, b1 = (c + 1) * nb / gridDim.x;
+    float acc[NE][NJ];
+    int g = -1;
+    auto flush = [&]() {
+        if (g < 0 || g >= na) return;
+        float* out = slots + (c + g) * (int64_t)n * r;
+#pragma unroll
+        for (int a = 0; a < NE; ++a)
+#pragma unroll
+            for (int b = 0; b < NJ; ++b) {
+                const int e = te + 32 * a, j = tj + 8 * b;
+                if (e < n && j < r) out[e * r + j] = acc[a][b];
+            }
+    };
+    for (int64_t blk = b0; blk < b1; ++blk) {
+        const int64_t p0 = blk * kRows;
+        int ng = g < 0 ? atc_group(plan.goff, na + 1, (int)p0) : g;
+        while ((int64_t)plan.goff[ng + 1] <= p0) ++ng;
+        __syncthreads();  // the block before is done with the tiles
+        if (ng != g) {
+            flush();
+            g = ng;
+#pragma unroll
+            for (int a = 0; a < NE; ++a)
+#pragma unroll
+                for (int b = 0; b < NJ; ++b) acc[a][b] = 0.f;
+            if (g < na)
+                for (int i = tid; i < n * r; i += kThreads)
+                    sb[i / r * us + i % r] = __bfloat162float(bmat[(int64_t)g * n * r + i]);
+        }
+        if (tid < kRows) rows[tid] = plan.perm[p0 + tid];
+        __syncthreads();
+        for (int i = tid; i < kRows * n; i += kThreads) {
+            const int q = i / n, e = i - q * n;
+            sh[q * hs + e] = rows[q] >= 0 ? dh[(int64_t)rows[q] * n + e] : 0.f;
+        }
+        if (g < na)
+            for (int i = tid; i < kRows * r; i += kThreads) {
+                const int q = i / r, j = i - q * r;
+                su[q * us + j] = rows[q] >= 0 ? hidden[(int64_t)rows[q] * r + j] : 0.f;
+            }
+        __syncthreads();
+        for (int i = tid; i < kRows * nk; i += kThreads) {
+            const int q = i / nk, e = i - q * nk;
+            __nv_bfloat16 p[3];
+            split3(e < n ? sh[q * hs + e] : 0.f, p);
+            for (int k = 0; k < planes; ++k) dhp[((int64_t)k * mp + p0 + q) * nk + e] = p[k];
+        }
+        if (g >= na) continue;
+        const float s = scale[g];
+        for (int i = tid; i < kRows * rp; i += kThreads) {
+            const int q = i / rp, j = i - q * rp;
+            float t = 0.f;
+            if (j < r) {
+                for (int e = 0; e < n; ++e) t = fmaf(sh[q * hs + e], sb[e * us + j], t);
+                t *= s;
+            }
+            __nv_bfloat16 p[3];
+            split3(t, p);
+            __nv_bfloat16* o = dup + (p0 + q) * pc + j;
+            o[0] = p[0];
+            o[rp] = p[1];
+            o[2 * rp] = p[2];
+        }
+        float part[NE][NJ];
+#pragma unroll
+        for (int a = 0; a < NE; ++a)
+#pragma unroll
+            for (int b = 0; b < NJ; ++b) part[a][b] = 0.f;
+        for (int q = 0; q < kRows; ++q) {
+            float hv[NE], uv[NJ];
+#pragma unroll
+            for (int a = 0; a < NE; ++a) hv[a] = te + 32 * a < n ? sh[q * hs + te + 32 * a] : 0.f;
+#pragma unroll
+            for (int b = 0; b < NJ; ++b) uv[b] = tj + 8 * b < r ? su[q * us + tj + 8 * b] : 0.f;
+#pragma unroll
+            for (int a = 0; a < NE; ++a)
+#pragma unroll
+                for (int b = 0; b < NJ; ++b) part[a][b] = fmaf(hv[a], uv[b], part[a][b]);
+        }
+#pragma unroll
+        for (int a = 0; a < NE; ++a)
+#pragma unroll
+            for (int b = 0; b < NJ; ++b) acc[a][b] += part[a][b];
+    }
+    flush();
+}
+
+// db[g] = s_g * the group's slots, in CTA order; da[g] = 0 for a group without rows.
+__global__ void __launch_bounds__(asp::kThreads)
+adapters_fold_kernel(const float* __restrict__ slots, int n, int r, int d, int na, AdapterPlan plan,
+                     const float* __restrict__ scale, float* __restrict__ db, float* __restrict__ da) {
+    using namespace asp;
+    pdl_trigger();
+    pdl_wait();
+    const int g = blockIdx.y;
+    const int64_t per = (int64_t)n * r;
+    const int64_t nb = plan.goff[na + 1] / kRows, b0 = plan.goff[g] / kRows, b1 = plan.goff[g + 1] / kRows;
+    const int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
+    if (b1 == b0) {
+        for (int64_t i = i0; i < per; i += step) db[g * per + i] = 0.f;
+        for (int64_t i = i0; i < (int64_t)r * d; i += step) da[(int64_t)g * r * d + i] = 0.f;
+        return;
+    }
+    const int64_t cf = ((b0 + 1) * kGrid + nb - 1) / nb - 1, cl = (b1 * kGrid + nb - 1) / nb - 1;
+    for (int64_t i = i0; i < per; i += step) {
+        float t = 0.f;
+        for (int64_t c = cf; c <= cl; ++c)
+            if ((c + 1) * nb / kGrid > c * nb / kGrid) t += slots[(c + g) * per + i];  // with few blocks some CTAs have none
+        db[g * per + i] = scale[g] * t;
+    }
+}
+
+// ---------------------------------------------------------------- dx
+namespace adx {
+constexpr int kThreads = 384, kStages = 3;
+}
+
+struct AdxShared {
+    uint64_t full[adx::kStages], empty[adx::kStages], afull, aempty, tfull[2], tempty[2];
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+// MH: 128-row halves of a row tile; ND: columns of d at a time; NC: 64-column chunks of dh; RP: padded rank.
+template <int MH, int ND, int NC, int RP>
+struct AdxTile {
+    static constexpr int DH_BYTES = 2 * NC * MH * 16384;        // [plane][chunk][rows] of 128 bytes
+    static constexpr int DU_CHUNKS = RP / 32;                   // [hi | lo] in one chunk for rank 32, else one each
+    static constexpr int A_BYTES = DH_BYTES + DU_CHUNKS * MH * 16384;
+    static constexpr int STAGE = 2 * ND * 128;                  // both parts of W_r, or A_a
+    static constexpr int GC = MH == 2 ? ND : ND / 2;            // columns of an epilogue warp
+    static constexpr int CW = GC < 64 ? GC : 64;                // columns it stores at a time
+    static constexpr int OUT_BYTES = 8 * 32 * CW * 2;
+    static constexpr size_t SMEM = 1024 + A_BYTES + adx::kStages * STAGE + OUT_BYTES + sizeof(AdxShared);
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(2 * MH * ND <= 512, "two accumulators fit the TMEM");
+    static_assert(ND / 64 * RP * 128 <= STAGE, "A_a fits a stage");
+};
+
+// One unit = a row tile (256 grouped rows, or a half of them for MH = 1) x ND columns of d; the units of a
+// row tile follow one another, and the line of units is cut evenly over the CTAs.
+//   warp 0 TMA, warp 1 MMA, warps 4-11 TMEM -> bf16 -> shared memory -> whole 128-byte pieces of dx rows
+template <int MH, int ND, int NC, int RP>
+__global__ void __launch_bounds__(adx::kThreads, 1)
+adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_constant__ CUtensorMap map_du,
+                      const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, int d, int n,
+                      int r, int na, AdapterPlan plan, __nv_bfloat16* __restrict__ dx) {
+    using namespace adx;
+    using T = AdxTile<MH, ND, NC, RP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sa = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* su = sa + T::DH_BYTES;
+    uint8_t* ring = sa + T::A_BYTES;
+    uint8_t* outs = ring + kStages * T::STAGE;
+    AdxShared* sh = reinterpret_cast<AdxShared*>(outs + T::OUT_BYTES);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) { ptx::mbar_init(&sh->full[s], 1); ptx::mbar_init(&sh->empty[s], 1); }
+        ptx::mbar_init(&sh->afull, 1);
+        ptx::mbar_init(&sh->aempty, 1);
+        for (int b = 0; b < 2; ++b) { ptx::mbar_init(&sh->tfull[b], 1); ptx::mbar_init(&sh->tempty[b], 256); }
+        sh->abort_flag = 0;
+        ptx::fence_barrier_init();
+        ptx::prefetch_tensormap(&map_dh);
+        ptx::prefetch_tensormap(&map_du);
+        ptx::prefetch_tensormap(&map_w);
+        ptx::prefetch_tensormap(&map_a);
+    }
+    if (warp == 1) ptx::tmem_alloc(&sh->tmem_base, 2 * MH * ND);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t tmem = sh->tmem_base;
+    volatile int* abort_flag = &sh->abort_flag;
+    constexpr int SUB = MH == 1 ? 2 : 1;
+    const int groups = na + 1, ndc = (d + ND - 1) / ND;
+    const int64_t total = (int64_t)plan.tstart[groups] * SUB * ndc;
+    const int64_t lo = blockIdx.x * total / gridDim.x, hi = (blockIdx.x + 1) * total / gridDim.x;
+
+    // row tile -> group, first grouped position, rows (0: nothing to do)
+    auto rows_of = [&](int64_t tile, int& g, int& p0) -> int {
+        const int t = (int)(tile / SUB);
+        g = atc_group(plan.tstart, groups, t);
+        p0 = plan.goff[g] + 256 * (t - plan.tstart[g]) + 128 * (int)(tile % SUB);
+        const int cnt = plan.goff[g] + plan.gcnt[g] - p0;
+        return cnt < 0 ? 0 : min(cnt, 128 * MH);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, aphase = 0;
+            int64_t held = -1;
+            int g = 0, p0 = 0, cnt = 0;
+            bool ok = true;
+            for (int64_t u = lo; ok && u < hi; ++u) {
+                const int64_t tile = u / ndc;
+                const int d0 = (int)(u - tile * ndc) * ND;
+                if (tile != held) {
+                    held = tile;
+                    cnt = rows_of(tile, g, p0);
+                    if (cnt > 0) {
+                        const int halves = cnt > 128 ? 2 : 1;
+                        ok = ptx::mbar_wait(&sh->aempty, aphase ^ 1u, abort_flag);
+                        if (!ok) break;
+                        aphase ^= 1u;
+                        ptx::mbar_expect_tx(&sh->afull, (uint32_t)(halves * 16384 * (2 * NC + (g < na ? T::DU_CHUNKS : 0))));
+                        for (int h = 0; h < halves; ++h) {
+                            for (int p = 0; p < 2; ++p)
+                                for (int c = 0; c < NC; ++c)
+                                    ptx::tma_load_3d(sa + ((p * NC + c) * MH + h) * 16384, &map_dh, &sh->afull, 64 * c, p0 + 128 * h, p);
+                            if (g < na)
+                                for (int c = 0; c < T::DU_CHUNKS; ++c)
+                                    ptx::tma_load_2d(su + (c * MH + h) * 16384, &map_du, &sh->afull, 64 * c, p0 + 128 * h);
+                        }
+                    }
+                }
+                if (cnt == 0) continue;
+                for (int c = 0; c < NC + (g < na ? 1 : 0); ++c) {
+                    ok = ptx::mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag);
+                    if (!ok) break;
+                    uint8_t* st = ring + stage * T::STAGE;
+                    if (c < NC) {
+                        ptx::mbar_expect_tx(&sh->full[stage], 2 * ND * 128);
+                        for (int p = 0; p < 2; ++p) ptx::tma_load_3d(st + p * ND * 128, &map_w, &sh->full[stage], 64 * c, d0, p);
+                    } else {
+                        ptx::mbar_expect_tx(&sh->full[stage], ND / 64 * RP * 128);
+                        for (int q = 0; q < ND / 64; ++q)
+                            ptx::tma_load_3d(st + q * RP * 128, &map_a, &sh->full[stage], d0 + 64 * q, 0, g);
+                    }
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, ND);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, aphase = 0, bphase = 0;
+            int64_t held = -1;
+            int g = 0, p0 = 0, cnt = 0;
+            bool ok = true;
+            for (int64_t u = lo; ok && u < hi; ++u) {
+                const int64_t tile = u / ndc;
+                if (tile != held) {
+                    if (held >= 0 && cnt > 0) ptx::umma_commit(&sh->aempty);  // the tile before has been read
+                    held = tile;
+                    cnt = rows_of(tile, g, p0);
+                    if (cnt > 0) {
+                        ok = ptx::mbar_wait(&sh->afull, aphase, abort_flag);
+                        if (!ok) break;
+                        aphase ^= 1u;
+                    }
+                }
+                if (cnt == 0) continue;
+                const int halves = cnt > 128 ? 2 : 1;
+                ok = ptx::mbar_wait(&sh->tempty[buf], bphase ^ 1u, abort_flag);
+                if (!ok) break;
+                for (int c = 0; c < NC + (g < na ? 1 : 0); ++c) {
+                    ok = ptx::mbar_wait(&sh->full[stage], phase, abort_flag);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t st = ptx::smem_u32(ring + stage * T::STAGE);
+                    for (int h = 0; h < halves; ++h) {
+                        const uint32_t acc = tmem + (uint32_t)((buf * MH + h) * ND);
+                        if (c < NC) {
+                            const int steps = min(4, (n - 64 * c + 15) / 16);
+                            const uint64_t ahi = ptx::sw128_kmajor_desc(ptx::smem_u32(sa + (c * MH + h) * 16384));
+                            const uint64_t alo = ptx::sw128_kmajor_desc(ptx::smem_u32(sa + ((NC + c) * MH + h) * 16384));
+                            const uint64_t bhi = ptx::sw128_kmajor_desc(st), blo = ptx::sw128_kmajor_desc(st + ND * 128);
+                            for (int k = 0; k < steps; ++k) ptx::umma_bf16(acc, ahi + 2 * k, bhi + 2 * k, idesc, (c | k) != 0);
+                            for (int k = 0; k < steps; ++k) ptx::umma_bf16(acc, alo + 2 * k, bhi + 2 * k, idesc, 1u);
+                            for (int k = 0; k < steps; ++k) ptx::umma_bf16(acc, ahi + 2 * k, blo + 2 * k, idesc, 1u);
+                        } else {
+                            const int steps = (r + 15) / 16;
+                            const uint32_t ua = ptx::smem_u32(su + h * 16384);
+                            const uint64_t uhi = ptx::sw128_kmajor_desc(ua);
+                            const uint64_t ulo = RP == 32 ? uhi + 4 : ptx::sw128_kmajor_desc(ua + MH * 16384);
+                            const uint64_t bd = sw128_mnmajor_desc(st, RP * 128);
+                            for (int k = 0; k < steps; ++k) ptx::umma_bf16(acc, uhi + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
+                            for (int k = 0; k < steps; ++k) ptx::umma_bf16(acc, ulo + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
+                        }
+                    }
+                    ptx::umma_commit(&sh->empty[stage]);
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                }
+                ptx::umma_commit(&sh->tfull[buf]);
+                if (++buf == 2) { buf = 0; bphase ^= 1u; }
+            }
+        }
+    } else if (warp >= 4) {
+        const int quad = warp & 3, grp = (warp - 4) >> 2;
+        const int half = MH == 2 ? grp : 0, col0 = MH == 2 ? 0 : grp * T::GC;
+        uint8_t* mine = outs + (warp - 4) * 32 * T::CW * 2;  // [32][CW] bf16, 16-byte pieces swizzled by row
+        constexpr int PIECES = T::CW / 8;                    // 8 (or 4) pieces a row
+        int buf = 0;
+        uint32_t bphase = 0;
+        int64_t held = -1;
+        int g = 0, p0 = 0, cnt = 0;
+        int32_t rows[PIECES];  // the rows that this lane stores: quad rows lane / PIECES + (32 / PIECES) i
+        for (int64_t u = lo; u < hi; ++u) {
+            const int64_t tile = u / ndc;
+            const int d0 = (int)(u - tile * ndc) * ND;
+            if (tile != held) {
+                held = tile;
+                cnt = rows_of(tile, g, p0);
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i) {
+                    const int q = half * 128 + quad * 32 + lane / PIECES + 32 / PIECES * i;
+                    rows[i] = q < cnt ? plan.perm[p0 + q] : -1;
+                }
+            }
+            if (cnt == 0) continue;
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sh->tfull[buf], bphase, abort_flag))) break;
+            ptx::tc_fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)((buf * MH + half) * ND + col0);
+            const bool any = half * 128 + quad * 32 < cnt;
+#pragma unroll
+            for (int w = 0; w < T::GC; w += T::CW) {
+                if (any) {
+                    uint32_t v[T::CW];
+#pragma unroll
+                    for (int q = 0; q < T::CW / 16; ++q)
+                        ptx::tmem_ld16_issue(acc + (uint32_t)(w + 16 * q), *reinterpret_cast<uint32_t(*)[16]>(v + 16 * q));
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[8 * p + 2 * q]), __uint_as_float(v[8 * p + 2 * q + 1]));
+                            o[q] = *reinterpret_cast<const uint32_t*>(&b);
+                        }
+                        const int at = p ^ (PIECES == 8 ? (lane & 7) : ((lane >> 1) & 3));
+                        *reinterpret_cast<uint4*>(mine + (lane * PIECES + at) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                if (w + T::CW >= T::GC) {  // the accumulator is read
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&sh->tempty[buf]);
+                }
+                __syncwarp();
+                if (any) {
+                    const int piece = lane % PIECES, col = d0 + col0 + w + 8 * piece;
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i) {
+                        const int q = lane / PIECES + 32 / PIECES * i;
+                        const int at = piece ^ (PIECES == 8 ? (q & 7) : ((q >> 1) & 3));
+                        const uint4 t = *reinterpret_cast<const uint4*>(mine + (q * PIECES + at) * 16);
+                        if (rows[i] >= 0 && col < d) *reinterpret_cast<uint4*>(dx + (int64_t)rows[i] * d + col) = t;
+                    }
+                }
+                __syncwarp();
+            }
+            if (++buf == 2) { buf = 0; bphase ^= 1u; }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 2 * MH * ND);
+    }
+}
+
+// ---------------------------------------------------------------- contraction over rows
+namespace rct {
+constexpr int kThreads = 384, kDrain = 4, kMinRun = 4, BD = 256, BK = adp::kPad;
+}
+
+struct RctShared {
+    uint64_t full[4], empty[4], tfull, tempty;
+    uint32_t tmem_base;
+    int abort_flag, last;
+};
+
+// C columns of the other operand, in three bf16 parts: [p0 | p1], [p2] in chunks of 64 for C = 32, one
+// chunk each for C = 64.
+template <int C>
+struct RctTile {
+    static constexpr int CHUNKS = C == 32 ? 2 : 3;
+    static constexpr int X_BYTES = 4 * rct::BK * 128, STAGE = X_BYTES + CHUNKS * rct::BK * 128;
+    static constexpr int STAGES = 3, ACOLS = 3 * C;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + sizeof(RctShared);
+};
+
+// out[g][c][dd] (strides gs, cs, ds) = sum over the grouped positions p of group g of P[p][c] x[perm[p]][dd].
+// A unit is (group, 256 columns of d, C columns of P); its K blocks are the group's blocks of 64 positions.
+// `one`: all positions are one group. The line of K blocks is cut evenly over the CTAs, and a unit that a cut
+// divides is finished by the last of its CTAs to arrive, in CTA order, as in router_adapters_tc_kernel.
+// Padding positions have zero parts; their x rows are copies of a row of the same block, so that no other
+// group's row (which might hold a NaN) meets a zero.
+template <int C>
+__global__ void __launch_bounds__(rct::kThreads, 1)
+rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
+                        const __grid_constant__ CUtensorMap map_p, int d, int ncols, int na, int one, AdapterPlan plan,
+                        float* __restrict__ part, int32_t* __restrict__ tickets, float* __restrict__ out, int64_t gs,
+                        int64_t cs, int64_t ds) {
+    using namespace rct;
+    using T = RctTile<C>;
+    constexpr int STAGES = T::STAGES, ACOLS = T::ACOLS;
+    constexpr uint32_t TCOLS = 2 * ACOLS <= 256 ? 256 : 512;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    RctShared* sh = reinterpret_cast<RctShared*>(smem + STAGES * T::STAGE);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) { ptx::mbar_init(&sh->full[s], 3); ptx::mbar_init(&sh->empty[s], 1); }
+        ptx::mbar_init(&sh->tfull, 1);
+        ptx::mbar_init(&sh->tempty, 256);
+        sh->abort_flag = 0;
+        ptx::fence_barrier_init();
+        ptx::prefetch_tensormap(&map_x);
+        ptx::prefetch_tensormap(&map_g);
+        ptx::prefetch_tensormap(&map_p);
+    }
+    if (warp == 1) ptx::tmem_alloc(&sh->tmem_base, TCOLS);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t tmem = sh->tmem_base;
+    volatile int* abort_flag = &sh->abort_flag;
+    const int ndt = (d + BD - 1) / BD, nct = (ncols + C - 1) / C, U = ndt * nct;
+    const int64_t total = (int64_t)(plan.goff[one ? na + 1 : na] / BK) * U;
+    int64_t ctas = total / kMinRun;
+    ctas = ctas < 1 ? 1 : (ctas > gridDim.x ? gridDim.x : ctas);
+    const int64_t c = blockIdx.x;
+    const int64_t lo = c < ctas ? c * total / ctas : total, hi = c < ctas ? (c + 1) * total / ctas : total;
+
+    struct Unit {
+        int g, dt, ct, blk0, nkb;  // blk0: the group's first block of 64 positions
+        int64_t u0;                // the unit's first place on the line
+    };
+    auto unit_at = [&](int64_t pos) -> Unit {
+        Unit u;
+        u.g = 0;
+        u.blk0 = 0;
+        if (one) {
+            u.nkb = plan.goff[na + 1] / BK;
+        } else {
+            u.g = atc_group(plan.goff, na, (int)(pos / U) * BK);  // the last group that starts there: not empty
+            u.blk0 = plan.goff[u.g] / BK;
+            u.nkb = plan.goff[u.g + 1] / BK - u.blk0;
+        }
+        const int64_t in = pos - (int64_t)u.blk0 * U;
+        const int q = (int)(in / u.nkb);
+        u.dt = q / nct;
+        u.ct = q % nct;
+        u.u0 = (int64_t)u.blk0 * U + (int64_t)q * u.nkb;
+        return u;
+    };
+
+    if (warp < 4) {
+        ptx::regs_less<72>();
+        if (warp != 1) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t pos = lo; ok && pos < hi;) {
+                const Unit u = unit_at(pos);
+                const int kb0 = (int)(pos - u.u0), kb1 = (int)min((int64_t)u.nkb, kb0 + (hi - pos));
+                const int slab = warp & 1, quad = lane & 7, chunk = lane >> 3;  // warps 2, 3: slab 0, 1
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    const int p0 = (u.blk0 + kb) * BK;
+                    const int first0 = plan.perm[p0], last0 = plan.perm[p0 + 31];
+                    const int first1 = plan.perm[p0 + 32], last1 = plan.perm[p0 + 63];
+                    const bool run0 = last0 >= 0 && last0 - first0 == 31, run1 = last1 >= 0 && last1 - first1 == 31;
+                    const bool gather = warp >= 2 && !(slab == 0 ? run0 : run1);
+                    int rid[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int v = gather ? plan.perm[p0 + 32 * slab + 4 * quad + q] : 0;
+                        rid[q] = v < 0 ? first0 : v;
+                    }
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag));
+                    if (!ok) break;
+                    uint8_t* st = smem + stage * T::STAGE;
+                    uint64_t* bar = &sh->full[stage];
+                    // each of the three warps announces its own bytes, also none: a warp that a stage did not wait
+                    // for could fall a whole ring behind and then wait for a phase that has passed
+                    if (lane == 0)
+                        ptx::mbar_expect_tx(bar, warp == 0 ? T::CHUNKS * BK * 128 + ((run0 ? 4 : 0) + (run1 ? 4 : 0)) * 4096
+                                                           : (gather ? 16384 : 0));
+                    __syncwarp();
+                    if (warp == 0) {
+                        if (lane < 8 && ((lane & 1) == 0 ? run0 : run1))  // chunk lane / 2, slab lane & 1
+                            ptx::tma_load_2d(st + (lane >> 1) * BK * 128 + (lane & 1) * 4096, &map_x, bar,
+                                             u.dt * BD + 64 * (lane >> 1), (lane & 1) == 0 ? first0 : first1);
+                        if (lane >= 8 && lane < 8 + T::CHUNKS) {
+                            const int q = lane - 8;
+                            // dh: a plane per part; du: the parts beside one another
+                            ptx::tma_load_3d(st + T::X_BYTES + q * BK * 128, &map_p, bar, one ? C * u.ct : 64 * q, p0, one ? q : 0);
+                        }
+                    } else if (gather) {
+                        tma_gather4(st + chunk * BK * 128 + slab * 4096 + quad * 512, &map_g, bar, u.dt * BD + 64 * chunk, rid[0],
+                                    rid[1], rid[2], rid[3]);
+                    }
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                pos += kb1 - kb0;
+            }
+        } else {
+            if (lane == 0) {
+                constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, ACOLS) | kIdescAMn | kIdescBMn;
+                int stage = 0;
+                uint32_t phase = 0, tphase = 0;
+                bool ok = true;
+                for (int64_t pos = lo; ok && pos < hi;) {
+                    const Unit u = unit_at(pos);
+                    const int kb0 = (int)(pos - u.u0), kb1 = (int)min((int64_t)u.nkb, kb0 + (hi - pos));
+                    const int halves = d - u.dt * BD > 128 ? 2 : 1;
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        const int in = (kb - kb0) % kDrain;
+                        if (in == 0) {
+                            ok = ptx::mbar_wait(&sh->tempty, tphase ^ 1u, abort_flag);
+                            if (!ok) break;
+                        }
+                        ok = ptx::mbar_wait(&sh->full[stage], phase, abort_flag);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint32_t st = ptx::smem_u32(smem + stage * T::STAGE);
+                        const uint64_t bdesc = sw128_mnmajor_desc(st + T::X_BYTES, BK * 128);
+                        for (int h = 0; h < halves; ++h) {
+                            const uint64_t adesc = sw128_mnmajor_desc(st + h * 2 * BK * 128, BK * 128);
+#pragma unroll
+                            for (int kk = 0; kk < BK / 16; ++kk)
+                                ptx::umma_bf16(tmem + (uint32_t)(h * ACOLS), adesc + 128 * kk, bdesc + 128 * kk, idesc,
+                                               (in != 0 || kk != 0) ? 1u : 0u);
+                        }
+                        ptx::umma_commit(&sh->empty[stage]);
+                        if (in == kDrain - 1 || kb == kb1 - 1) { ptx::umma_commit(&sh->tfull); tphase ^= 1u; }
+                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    }
+                    pos += kb1 - kb0;
+                }
+            }
+        }
+    } else {
+        ptx::regs_more<216>();
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const int row = half * 128 + quad * 32 + lane;  // column of the d tile
+        const int et = tid - 128;
+        const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * ACOLS);
+        uint32_t tphase = 0;
+        bool ok = true;
+        for (int64_t pos = lo; pos < hi;) {
+            const Unit u = unit_at(pos);
+            const int kb0 = (int)(pos - u.u0), kb1 = (int)min((int64_t)u.nkb, kb0 + (hi - pos));
+            const int dd = u.dt * BD + row;
+            const bool mine = u.dt * BD + half * 128 < d;
+            float acc[C];
+#pragma unroll
+            for (int j = 0; j < C; ++j) acc[j] = 0.f;
+            for (int kb = kb0; kb < kb1; kb += kDrain) {
+                // after a give-up every warp still walks its loops: the barriers below count them all
+                if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->tfull, tphase, abort_flag));
+                tphase ^= 1u;
+                if (!ok) continue;
+                ptx::tc_fence_after();
+                if (mine) {
+#pragma unroll
+                    for (int q = 0; q < C / 16; ++q) {
+                        uint32_t v[3][16];
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) ptx::tmem_ld16_issue(trow + (uint32_t)(p * C + q * 16), v[p]);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            acc[q * 16 + j] = __fadd_rn(acc[q * 16 + j], __fadd_rn(__fadd_rn(__uint_as_float(v[2][j]), __uint_as_float(v[1][j])),
+                                                                                   __uint_as_float(v[0][j])));
+                    }
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&sh->tempty);
+            }
+            bool finish = true;
+            if (kb0 != 0 || kb1 != u.nkb) {
+                float* mp = part + (2 * c + (kb0 == 0 ? 1 : 0)) * (int64_t)C * BD + row;
+                if (ok && mine) {
+#pragma unroll
+                    for (int j = 0; j < C; ++j) __stcg(mp + (int64_t)j * BD, acc[j]);
+                }
+                __threadfence();
+                ptx::named_barrier(1, 256);
+                const int64_t cf = ((u.u0 + 1) * ctas + total - 1) / total - 1;
+                const int64_t cl = ((u.u0 + u.nkb) * ctas + total - 1) / total - 1;
+                if (et == 0) sh->last = atomicAdd(tickets + (int64_t)u.g * U + u.dt * nct + u.ct, 1) == (int)(cl - cf);
+                ptx::named_barrier(1, 256);
+                finish = sh->last != 0;
+                if (finish) {
+                    __threadfence();
+#pragma unroll
+                    for (int j = 0; j < C; ++j) acc[j] = 0.f;
+                    if (mine) {
+                        for (int64_t cc = cf; cc <= cl; ++cc) {
+                            const int64_t at = cc * total / ctas;  // where the CTA's run begins
+                            const float* op = part + (2 * cc + (at <= u.u0 ? 1 : 0)) * (int64_t)C * BD + row;
+#pragma unroll
+                            for (int j = 0; j < C; ++j) acc[j] = __fadd_rn(acc[j], __ldcg(op + (int64_t)j * BD));
+                        }
+                    }
+                }
+            }
+            if (finish && ok && dd < d) {
+                float* o = out + u.g * gs + (int64_t)u.ct * C * cs + dd * ds;
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+                    if (u.ct * C + j < ncols) o[j * cs] = acc[j];
+            }
+            pos += kb1 - kb0;
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, TCOLS);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+struct AgtWs {
+    AdapterPlan plan;
+    __nv_bfloat16 *wparts;  // [2, d, nk]
+    __nv_bfloat16 *dhp;     // [3, m_pad, nk]
+    __nv_bfloat16 *dup;     // [m_pad, pc]
+    float *slots;           // [grid + na][n, r]
+    float *part;            // [2 kNumSMs][64][256]
+    int32_t *tickets;       // one per unit of the two contractions
+};
+
+struct AgtShape {
+    int nk, rp, pc, ndt, nct;
+    int64_t mp, tickets_a, tickets_w;
+};
+
+static AgtShape agt_shape(int64_t m, int d, int n, int r, int na) {
+    AgtShape s;
+    s.nk = (n + 7) / 8 * 8;
+    s.rp = r <= 32 ? 32 : 64;
+    s.pc = r <= 32 ? 128 : 192;
+    s.ndt = (d + rct::BD - 1) / rct::BD;
+    s.nct = (n + 63) / 64;
+    s.mp = adapter_padded_rows(m, na);
+    s.tickets_a = (int64_t)na * s.ndt;
+    s.tickets_w = (int64_t)s.ndt * s.nct;
+    return s;
+}
+
+static size_t agt_layout(int64_t m, int d, int n, int r, int na, AgtWs* w, char* base) {
+    const AgtShape s = agt_shape(m, d, n, r, na);
+    size_t off = adapter_plan_layout(m, na, w ? &w->plan : nullptr, base);
+    auto take = [&](size_t bytes) { char* p = base + off; off += (bytes + 255) & ~size_t(255); return p; };
+    char* p;
+    p = take((size_t)2 * d * s.nk * 2);                         if (w) w->wparts = (__nv_bfloat16*)p;
+    p = take((size_t)3 * s.mp * s.nk * 2);                      if (w) w->dhp = (__nv_bfloat16*)p;
+    p = take((size_t)s.mp * s.pc * 2);                          if (w) w->dup = (__nv_bfloat16*)p;
+    p = take((size_t)(asp::kGrid + na) * n * r * 4);            if (w) w->slots = (float*)p;
+    p = take((size_t)2 * kNumSMs * 64 * rct::BD * 4);           if (w) w->part = (float*)p;
+    p = take((size_t)(s.tickets_a + s.tickets_w) * 4);          if (w) w->tickets = (int32_t*)p;
+    return off;
+}
+
+// set on every call: the attribute belongs to the current device
+template <typename K>
+static cudaError_t need_smem(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <int MH, int ND, int NC, int RP>
+static cudaError_t launch_adx(const CUtensorMap& mdh, const CUtensorMap& mdu, const CUtensorMap& mw,
+                              const CUtensorMap& ma, int d, int n, int r, int na, const AdapterPlan& plan,
+                              __nv_bfloat16* dx, cudaStream_t stream) {
+    constexpr size_t smem = AdxTile<MH, ND, NC, RP>::SMEM;
+    const cudaError_t e = need_smem(adapters_dx_tc_kernel<MH, ND, NC, RP>, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(adapters_dx_tc_kernel<MH, ND, NC, RP>, dim3(kNumSMs), dim3(adx::kThreads), smem, stream, mdh, mdu,
+                      mw, ma, d, n, r, na, plan, dx);
+}
+
+template <int C>
+static cudaError_t launch_rct(const CUtensorMap& mx, const CUtensorMap& mg, const CUtensorMap& mp, int d, int ncols,
+                              int na, int one, const AdapterPlan& plan, float* part, int32_t* tickets, float* out,
+                              int64_t gs, int64_t cs, int64_t ds, cudaStream_t stream) {
+    constexpr size_t smem = RctTile<C>::SMEM;
+    const cudaError_t e = need_smem(rows_contract_tc_kernel<C>, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(rows_contract_tc_kernel<C>, dim3(kNumSMs), dim3(rct::kThreads), smem, stream, mx, mg, mp, d, ncols,
+                      na, one, plan, part, tickets, out, gs, cs, ds);
+}
+
+template <int NE, int NJ>
+static cudaError_t launch_split(const float* dh, const float* hidden, const __nv_bfloat16* b, const float* scale, int n,
+                                int r, int na, const AgtShape& s, const AgtWs& w, int planes, cudaStream_t stream) {
+    const size_t smem = sizeof(float) * ((size_t)asp::kRows * ((n | 1) + (r | 1)) + (size_t)n * (r | 1));
+    const cudaError_t e = need_smem(adapters_split_kernel<NE, NJ>, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(adapters_split_kernel<NE, NJ>, dim3(asp::kGrid), dim3(asp::kThreads), smem, stream, dh, hidden, b,
+                      scale, n, r, na, w.plan, s.nk, planes, s.mp, w.dhp, s.pc, s.rp, w.dup, w.slots);
+}
+
+static cudaError_t launch_adapters_grad_tc(const float* dh, const __nv_bfloat16* x, const float* w_r,
+                                           const __nv_bfloat16* a, const __nv_bfloat16* b, const int32_t* idx,
+                                           const float* scale, const float* hidden, int64_t m, int d, int n, int r,
+                                           int na, __nv_bfloat16* dx, float* da, float* db, float* dw_r,
+                                           void* workspace, cudaStream_t stream) {
+    const AgtShape s = agt_shape(m, d, n, r, na);
+    AgtWs w;
+    agt_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
+    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, w.tickets, s.tickets_a + s.tickets_w, w_r, d, n, s.nk, 2,
+                                        dx ? w.wparts : nullptr, stream);
+    if (e != cudaSuccess) return e;
+    const int planes = dw_r ? 3 : 2;
+#define MOE_SPLIT(NE, NJ) e = launch_split<NE, NJ>(dh, hidden, b, scale, n, r, na, s, w, planes, stream)
+#define MOE_SPLIT_R(NE) do { if (r <= 16) MOE_SPLIT(NE, 2); else if (r <= 32) MOE_SPLIT(NE, 4); else MOE_SPLIT(NE, 8); } while (0)
+    if (n <= 64) MOE_SPLIT_R(2);
+    else if (n <= 128) MOE_SPLIT_R(4);
+    else MOE_SPLIT_R(8);
+#undef MOE_SPLIT_R
+#undef MOE_SPLIT
+    if (e != cudaSuccess) return e;
+    CUtensorMap mx, mg, ma, mw, mdh, mdu, mpw, mpa;
+    if (!map_2d(&mx, x, (uint64_t)m, (uint64_t)d, 32) || !map_2d(&mg, x, (uint64_t)m, (uint64_t)d, 1) ||
+        !map_3d(&mpa, w.dup, 1, (uint64_t)s.mp, (uint64_t)s.pc, rct::BK) ||
+        !map_3d(&mpw, w.dhp, 3, (uint64_t)s.mp, (uint64_t)s.nk, rct::BK) ||
+        !map_3d(&ma, a, (uint64_t)na, (uint64_t)r, (uint64_t)d, (uint32_t)s.rp) ||
+        !map_3d(&mdh, w.dhp, 2, (uint64_t)s.mp, (uint64_t)s.nk, 128) ||
+        !map_2d(&mdu, w.dup, (uint64_t)s.mp, (uint64_t)s.pc, 128))
+        return cudaErrorInvalidValue;
+    if (dx) {
+        const int nd = n <= 128 ? 128 : 64;
+        if (!map_3d(&mw, w.wparts, 2, (uint64_t)d, (uint64_t)s.nk, (uint32_t)nd)) return cudaErrorInvalidValue;
+#define MOE_ADX(MH, ND, NC, RP) e = launch_adx<MH, ND, NC, RP>(mdh, mdu, mw, ma, d, n, r, na, w.plan, dx, stream)
+        if (n <= 64) { if (s.rp == 32) MOE_ADX(2, 128, 1, 32); else MOE_ADX(1, 128, 1, 64); }
+        else if (n <= 128) { if (s.rp == 32) MOE_ADX(1, 128, 2, 32); else MOE_ADX(1, 128, 2, 64); }
+        else { if (s.rp == 32) MOE_ADX(1, 64, 4, 32); else MOE_ADX(1, 64, 4, 64); }
+#undef MOE_ADX
+        if (e != cudaSuccess) return e;
+    }
+    if (s.rp == 32)
+        e = launch_rct<32>(mx, mg, mpa, d, r, na, 0, w.plan, w.part, w.tickets, da, (int64_t)r * d, d, 1, stream);
+    else
+        e = launch_rct<64>(mx, mg, mpa, d, r, na, 0, w.plan, w.part, w.tickets, da, (int64_t)r * d, d, 1, stream);
+    if (e != cudaSuccess) return e;
+    if (dw_r) {
+        e = launch_rct<64>(mx, mg, mpw, d, n, na, 1, w.plan, w.part, w.tickets + s.tickets_a, dw_r, 0, 1, n, stream);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t per = (int64_t)n * r;
+    return launch_pdl(adapters_fold_kernel, dim3((unsigned)((per + asp::kThreads - 1) / asp::kThreads), (unsigned)na),
+                      dim3(asp::kThreads), 0, stream, w.slots, n, r, d, na, w.plan, scale, db, da);
+}
+
+}  // namespace moe

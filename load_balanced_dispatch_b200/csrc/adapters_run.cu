@@ -9,19 +9,18 @@ size_t router_adapters_workspace_bytes(int64_t m, int32_t d, int32_t n, int32_t 
 }
 
 size_t router_adapters_grad_workspace_bytes(int64_t m, int32_t d, int32_t n, int32_t r, int32_t na, moe_dtype dt) {
-    (void)dt;
-    if (m < 0 || d < 1 || n < 1 || r < 1 || na < 1) return 0;
+    if (m < 1 || d < 1 || n < 1 || n > kMaxExperts || r < 1 || r > kMaxRank || na < 1) return 0;
+    if (dt == MOE_BF16) return agt_layout(m, d, n, r, na, nullptr, nullptr);
     return adapter_ws_layout(m, d, n, r, na, nullptr, nullptr);
 }
 
-template <typename T>
-static cudaError_t launch_adapters_rows(const T* x, const float* w_r, const T* a, const T* b, const int32_t* idx,
-                                        const float* scale, int64_t m, int d, int n, int r, int na, float* logits,
-                                        float* hidden, cudaStream_t stream) {
+static cudaError_t launch_adapters_rows(const float* x, const float* w_r, const float* a, const float* b,
+                                        const int32_t* idx, const float* scale, int64_t m, int d, int n, int r, int na,
+                                        float* logits, float* hidden, cudaStream_t stream) {
 #define MOE_ADAPTER_ROWS(NP)                                                                                       \
     do {                                                                                                           \
         constexpr int RG = adp::kThreads / NP, R = RG > 16 ? RG : 16;                                              \
-        return launch_pdl(adapters_rows_kernel<T, NP>, dim3((unsigned)((m + R - 1) / R)), dim3(adp::kThreads), 0,  \
+        return launch_pdl(adapters_rows_kernel<NP>, dim3((unsigned)((m + R - 1) / R)), dim3(adp::kThreads), 0,  \
                           stream, x, w_r, a, b, idx, scale, m, d, n, r, na, logits, hidden);                       \
     } while (0)
     if (n <= 8) MOE_ADAPTER_ROWS(8);
@@ -45,25 +44,22 @@ cudaError_t launch_router_adapters(const void* x, moe_dtype dt, const float* w_r
                                 static_cast<const float*>(b), idx, scale, m, d, n, r, na, logits, hidden, stream);
 }
 
-template <typename T>
-static cudaError_t launch_adapters_grad_t(const float* dh, const T* x, const float* w_r, const T* a, const T* b,
-                                          const int32_t* idx, const float* scale, const float* hidden, int64_t m,
-                                          int d, int n, int r, int na, T* dx, float* da, float* db, float* dw_r,
-                                          void* workspace, cudaStream_t stream) {
+static cudaError_t launch_adapters_grad_f32(const float* dh, const float* x, const float* w_r, const float* a,
+                                            const float* b, const int32_t* idx, const float* scale,
+                                            const float* hidden, int64_t m, int d, int n, int r, int na, float* dx,
+                                            float* da, float* db, float* dw_r, void* workspace, cudaStream_t stream) {
     AdapterWs w;
     adapter_ws_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
-    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, nullptr, 0, nullptr, 0, 0, nullptr, stream);
+    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, nullptr, 0, nullptr, 0, 0, 0, 0, nullptr, stream);
     if (e != cudaSuccess) return e;
-    if (m > 0) {
-        const int rows = adp::kThreads / 32;
-        e = launch_pdl(adapters_du_kernel<T>, dim3((unsigned)((m + rows - 1) / rows)), dim3(adp::kThreads), 0, stream,
-                       dh, b, idx, scale, m, n, r, na, w.du);
+    const int rows = adp::kThreads / 32;
+    e = launch_pdl(adapters_du_kernel, dim3((unsigned)((m + rows - 1) / rows)), dim3(adp::kThreads), 0, stream, dh, b,
+                   idx, scale, m, n, r, na, w.du);
+    if (e != cudaSuccess) return e;
+    if (dx) {
+        e = launch_pdl(adapters_dx_kernel, dim3((unsigned)((m + 15) / 16), (unsigned)((d + 127) / 128)),
+                       dim3(adp::kThreads), 0, stream, dh, w_r, a, idx, w.du, m, d, n, r, na, dx);
         if (e != cudaSuccess) return e;
-        if (dx) {
-            e = launch_pdl(adapters_dx_kernel<T>, dim3((unsigned)((m + 15) / 16), (unsigned)((d + 127) / 128)),
-                           dim3(adp::kThreads), 0, stream, dh, w_r, a, idx, w.du, m, d, n, r, na, dx);
-            if (e != cudaSuccess) return e;
-        }
     }
     e = launch_rows_contract(x, d, w.du, r, m, na, w.plan, nullptr, w.part, da, stream);
     if (e != cudaSuccess) return e;
@@ -77,14 +73,20 @@ cudaError_t launch_router_adapters_grad(const float* dh, const void* x, moe_dtyp
                                         const void* b, const int32_t* idx, const float* scale, const float* hidden,
                                         int64_t m, int d, int n, int r, int na, void* dx, float* da, float* db,
                                         float* dw_r, void* workspace, cudaStream_t stream) {
+    if (m == 0) {  // no rows: the sums are zero
+        cudaError_t e = cudaMemsetAsync(da, 0, sizeof(float) * (size_t)na * r * d, stream);
+        if (e == cudaSuccess) e = cudaMemsetAsync(db, 0, sizeof(float) * (size_t)na * n * r, stream);
+        if (e == cudaSuccess && dw_r) e = cudaMemsetAsync(dw_r, 0, sizeof(float) * (size_t)d * n, stream);
+        return e;
+    }
     if (dt == MOE_BF16)
-        return launch_adapters_grad_t(dh, static_cast<const __nv_bfloat16*>(x), w_r,
-                                      static_cast<const __nv_bfloat16*>(a), static_cast<const __nv_bfloat16*>(b), idx,
-                                      scale, hidden, m, d, n, r, na, static_cast<__nv_bfloat16*>(dx), da, db, dw_r,
-                                      workspace, stream);
-    return launch_adapters_grad_t(dh, static_cast<const float*>(x), w_r, static_cast<const float*>(a),
-                                  static_cast<const float*>(b), idx, scale, hidden, m, d, n, r, na,
-                                  static_cast<float*>(dx), da, db, dw_r, workspace, stream);
+        return launch_adapters_grad_tc(dh, static_cast<const __nv_bfloat16*>(x), w_r,
+                                       static_cast<const __nv_bfloat16*>(a), static_cast<const __nv_bfloat16*>(b), idx,
+                                       scale, hidden, m, d, n, r, na, static_cast<__nv_bfloat16*>(dx), da, db, dw_r,
+                                       workspace, stream);
+    return launch_adapters_grad_f32(dh, static_cast<const float*>(x), w_r, static_cast<const float*>(a),
+                                    static_cast<const float*>(b), idx, scale, hidden, m, d, n, r, na,
+                                    static_cast<float*>(dx), da, db, dw_r, workspace, stream);
 }
 
 }  // namespace moe

@@ -89,7 +89,7 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
     const int nkb = (d + BK - 1) / BK;
 
     if (tid == 0) {
-        for (int s = 0; s < STAGES; ++s) { ptx::mbar_init(&sh->full[s], 1); ptx::mbar_init(&sh->empty[s], 1); }
+        for (int s = 0; s < STAGES; ++s) { ptx::mbar_init(&sh->full[s], 3); ptx::mbar_init(&sh->empty[s], 1); }
         ptx::mbar_init(&sh->tfull, 1);
         ptx::mbar_init(&sh->tempty, 256);
         sh->abort_flag = 0;
@@ -151,17 +151,19 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                 int rid[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) rid[q] = gather ? plan.perm[p0 + min(quad + q, cnt - 1)] : 0;
-                uint32_t bytes = 3 * NP * 128 + (ad ? RP * 128 : 0) + __popc(boxes) * 4096;
-                for (int q = 0; q < 8; ++q)
-                    if (gathers >> q & 1u) bytes += (min(32, cnt - 32 * q) + 3) / 4 * 512;
+                // each of the three warps announces its own bytes, also none: a warp that a stage did not wait for
+                // could fall a whole ring behind and then wait for a phase that has passed
+                const uint32_t bytes = warp == 0 ? 3 * NP * 128 + (ad ? RP * 128 : 0) + __popc(boxes) * 4096
+                                                 : __popc(__ballot_sync(0xffffffffu, gather)) * 512;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag));
                     if (!ok) break;
                     uint8_t* st = smem + stage * T::STAGE;
                     uint8_t* sb = st + A_BYTES;
                     uint64_t* bar = &sh->full[stage];
+                    if (lane == 0) ptx::mbar_expect_tx(bar, bytes);
+                    __syncwarp();
                     if (warp == 0) {
-                        if (lane == 0) ptx::mbar_expect_tx(bar, bytes);
                         // B rows: fused [W0 W1 W2 A], else [W0 A W1 W2]
                         if (lane >= 8 && lane < 11) {
                             const int p = lane - 8;
@@ -438,7 +440,8 @@ static cudaError_t launch_router_adapters_tc(const __nv_bfloat16* x, const float
     atc_tile(n, r, np, rp, nct);
     AtcWs w;
     atc_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
-    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, w.tickets, atc_tiles(m, na) * nct, w_r, d, n, w.wsplit, stream);
+    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, w.tickets, atc_tiles(m, na) * nct, w_r, d, n, 0, 3, w.wsplit,
+                                       stream);
     if (e != cudaSuccess) return e;
     CUtensorMap mx, mg, mw, ma;
     if (!map_2d(&mx, x, (uint64_t)m, (uint64_t)d, 32) || !map_2d(&mg, x, (uint64_t)m, (uint64_t)d, 1) ||

@@ -575,3 +575,27 @@ def test_refusals_of_the_binding():
         lb.moe_combine_grad(dy, ybuf, dest, gate, dybuf=ybuf)
     with pytest.raises(ValueError):
         lb.moe_combine_grad(dy, ybuf.float(), dest, gate)
+
+
+@pytest.mark.parametrize("m,d,n,r,na,order", [(20000, 512, 64, 16, 7, "runs"), (9000, 640, 128, 40, 30, "mixed"),
+                                              (30, 2048, 64, 16, 24, "mixed"), (12000, 256, 32, 8, 3, "patches")])
+def test_calls_that_follow_one_another(m, d, n, r, na, order):
+    # nothing waits between the calls: a kernel's prologue overlaps the one before it, and slabs of rows that follow
+    # one another take turns with gathered ones
+    i, dh = adapter_inputs(m, d, n, r, na, torch.bfloat16, "runs" if order == "patches" else order, 51)
+    if order == "patches":
+        g = gen(52)
+        at = torch.randint(0, m, (60,), generator=g, device="cuda")
+        i["adapter_idx"][at] = torch.randint(-1, na, (60,), generator=g, device="cuda", dtype=torch.int32)
+    first = lb.moe_router_adapters(**i)
+    grads = lb.moe_router_adapters_grad(dh, hidden=first[1], want_dw_r=True, **i)
+    lb.sync_status()
+    outs = []
+    for _ in range(40):
+        f = lb.moe_router_adapters(**i)
+        outs.append((f, lb.moe_router_adapters_grad(dh, hidden=f[1], want_dw_r=True, **i)))
+        outs = outs[-3:]
+    lb.sync_status()
+    for f, b in outs:
+        for p, q in zip(f + b, first + grads):
+            assert torch.equal(p, q)
