@@ -10,6 +10,7 @@ import of any function raises immediately.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -524,53 +525,57 @@ def moe_balance_assign(s, k, beta=None, mode=MOE_QB_SOLVE, rule=MOE_QB_MIDPOINT,
 
 
 # ---------------------------------------------------------------- training the router, adapters per request
-class _on:
-    """Run a call on the device of its tensors and allocate what it needs on `stream` (so that freed
-    outputs and workspaces are reused in that stream's order)."""
+def _on_stream(fn):
+    """Run a call with the device of its first tensor current and, given `stream`, on that stream: what it allocates
+    is then freed and reused in that stream's order."""
+    name = fn.__code__.co_varnames[0]
 
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got {dev}")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        self.stack = []
-        if torch.cuda.current_device() != dev.index:
-            self.stack.append(torch.cuda.device(dev))
-        if stream is not None:
-            self.stack.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.stack:
-            c.__enter__()
-
-    def __exit__(self, *exc):
-        for c in reversed(self.stack):
-            c.__exit__(*exc)
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise ValueError(f"{fn.__name__}: {name} must be a CUDA tensor")
+        if stream is None:
+            if first.get_device() == torch.cuda.current_device():
+                return fn(*args, **kw)
+            with torch.cuda.device(first.device):
+                return fn(*args, **kw)
+        if stream.device != first.device:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {first.device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
-def _need_on(dev, t, dtype, shape, name):
-    """_need, and on `dev`; None is refused."""
-    if t is None:
-        raise ValueError(f"{name} is required")
-    _need(t, dtype, shape, name)
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+def _raw_stream(dev):
+    """The current stream of device `dev`, as the address that the library takes."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _chk(dev, t, dtype, shape, name):
+    """t is a contiguous tensor of this type and shape on CUDA device `dev`; its address."""
+    if t is None or t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        if t is None:
+            raise ValueError(f"{name} is required")
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def _out(dev, t, dtype, shape, name):
     """An output: the caller's tensor, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need_on(dev, t, dtype, shape, name)
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    _chk(dev, t, dtype, shape, name)
     return t
 
 
-def _work_on(dev, workspace, nbytes):
-    """A workspace: the caller's (the library checks its size) or a new one."""
+def _work(dev, workspace, size, *args):
+    """A workspace: the caller's (the library checks its size) or a new one of size(*args) bytes."""
     if workspace is None:
-        return torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=dev)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {dev}")
+        return torch.empty((max(size(*args), 1),), dtype=torch.uint8, device=torch.device("cuda", dev))
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace: expected a contiguous uint8 tensor on cuda:{dev}")
     return workspace
 
 
@@ -597,137 +602,123 @@ def moe_router_loss_workspace_size(m, n, nseq) -> int:
     return lib().moe_router_loss_workspace_size(m, n, nseq)
 
 
-def _adapter_shapes(x, w_r, a, b, adapter_idx, scale):
+def _adapter_args(x, w_r, a, b, adapter_idx, scale):
+    """The shared arguments, checked: (device, shapes, type, addresses in the library's order)."""
     m, d = x.shape
     n = w_r.shape[1]
-    na, r, _ = a.shape
-    dev = x.device
-    _dtype_code(x)
-    _need_on(dev, x, x.dtype, (m, d), "x")
-    _need_on(dev, w_r, torch.float32, (d, n), "w_r")
-    _need_on(dev, a, x.dtype, (na, r, d), "a")
-    _need_on(dev, b, x.dtype, (na, n, r), "b")
-    _need_on(dev, adapter_idx, torch.int32, (m,), "adapter_idx")
-    _need_on(dev, scale, torch.float32, (na,), "scale")
-    return m, d, n, r, na, dev
+    na, r = a.shape[:2]
+    dev, dt = x.get_device(), x.dtype
+    ptrs = (_chk(dev, x, dt, (m, d), "x"), _chk(dev, w_r, torch.float32, (d, n), "w_r"), _chk(dev, a, dt, (na, r, d), "a"),
+            _chk(dev, b, dt, (na, n, r), "b"), _chk(dev, adapter_idx, torch.int32, (m,), "adapter_idx"),
+            _chk(dev, scale, torch.float32, (na,), "scale"))
+    return dev, (m, d, n, r, na), _torch_dtype_code(dt), ptrs
 
 
-def moe_router_adapters(x, w_r, a, b, adapter_idx, scale, logits=None, hidden=None, want_hidden=True, workspace=None,
-                        stream=None):
+@_on_stream
+def moe_router_adapters(x, w_r, a, b, adapter_idx, scale, logits=None, hidden=None, want_hidden=True, workspace=None):
     """Router logits with a low-rank adapter per token beside the shared projection:
     logits_i = x_i W_r + scale_a B_a (A_a x_i), a = adapter_idx[i] (-1: none). a [na, r, d] and b [na, n, r] have
-    x's dtype. Returns (logits [m, n] fp32, hidden [m, r] fp32 = A_a x_i, kept for the backward, or None)."""
-    m, d, n, r, na, dev = _adapter_shapes(x, w_r, a, b, adapter_idx, scale)
-    dt = _dtype_code(x)
-    with _on(dev, stream):
-        logits = _out(dev, logits, torch.float32, (m, n), "logits")
-        if hidden is not None or want_hidden:
-            hidden = _out(dev, hidden, torch.float32, (m, r), "hidden")
-        workspace = _work_on(dev, workspace, lib().moe_router_adapters_workspace_size(m, d, n, r, na, dt))
-        _check("moe_router_adapters", lib().moe_router_adapters(
-            _ptr(x), dt, _ptr(w_r), _ptr(a), _ptr(b), _ptr(adapter_idx), _ptr(scale), m, d, n, r, na, _ptr(logits),
-            _ptr(hidden), _ptr(workspace), workspace.numel(), _stream(stream)))
+    x's dtype. Returns (logits [m, n] fp32, hidden [m, r] fp32 = A_a x_i, kept for the backward, or None).
+    `stream`: run there instead of on the current stream."""
+    dev, (m, d, n, r, na), dt, (px, pw, pa, pb, pi, ps) = _adapter_args(x, w_r, a, b, adapter_idx, scale)
+    L = lib()
+    logits = _out(dev, logits, torch.float32, (m, n), "logits")
+    if hidden is not None or want_hidden:
+        hidden = _out(dev, hidden, torch.float32, (m, r), "hidden")
+    workspace = _work(dev, workspace, L.moe_router_adapters_workspace_size, m, d, n, r, na, dt)
+    _check("moe_router_adapters", L.moe_router_adapters(
+        px, dt, pw, pa, pb, pi, ps, m, d, n, r, na, logits.data_ptr(), None if hidden is None else hidden.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(dev)))
     return logits, hidden
 
 
+@_on_stream
 def moe_router_adapters_grad(dlogits, x, w_r, a, b, adapter_idx, scale, hidden, dx=None, da=None, db=None, dw_r=None,
-                             want_dx=True, want_dw_r=False, workspace=None, stream=None):
+                             want_dx=True, want_dw_r=False, workspace=None):
     """Backward of moe_router_adapters. Returns (dx [m, d] in x's dtype or None, da [na, r, d] fp32,
     db [na, n, r] fp32, dw_r [d, n] fp32 or None)."""
-    m, d, n, r, na, dev = _adapter_shapes(x, w_r, a, b, adapter_idx, scale)
-    dt = _dtype_code(x)
-    _need_on(dev, dlogits, torch.float32, (m, n), "dlogits")
-    _need_on(dev, hidden, torch.float32, (m, r), "hidden")
-    with _on(dev, stream):
-        if dx is not None or want_dx:
-            dx = _out(dev, dx, x.dtype, (m, d), "dx")
-        da = _out(dev, da, torch.float32, (na, r, d), "da")
-        db = _out(dev, db, torch.float32, (na, n, r), "db")
-        if dw_r is not None or want_dw_r:
-            dw_r = _out(dev, dw_r, torch.float32, (d, n), "dw_r")
-        workspace = _work_on(dev, workspace, lib().moe_router_adapters_grad_workspace_size(m, d, n, r, na, dt))
-        _check("moe_router_adapters_grad", lib().moe_router_adapters_grad(
-            _ptr(dlogits), _ptr(x), dt, _ptr(w_r), _ptr(a), _ptr(b), _ptr(adapter_idx), _ptr(scale), _ptr(hidden), m,
-            d, n, r, na, _ptr(dx), _ptr(da), _ptr(db), _ptr(dw_r), _ptr(workspace), workspace.numel(),
-            _stream(stream)))
+    dev, (m, d, n, r, na), dt, (px, pw, pa, pb, pi, ps) = _adapter_args(x, w_r, a, b, adapter_idx, scale)
+    L = lib()
+    f32 = torch.float32
+    ph, pu = _chk(dev, dlogits, f32, (m, n), "dlogits"), _chk(dev, hidden, f32, (m, r), "hidden")
+    if dx is not None or want_dx:
+        dx = _out(dev, dx, x.dtype, (m, d), "dx")
+    da, db = _out(dev, da, f32, (na, r, d), "da"), _out(dev, db, f32, (na, n, r), "db")
+    if dw_r is not None or want_dw_r:
+        dw_r = _out(dev, dw_r, f32, (d, n), "dw_r")
+    workspace = _work(dev, workspace, L.moe_router_adapters_grad_workspace_size, m, d, n, r, na, dt)
+    _check("moe_router_adapters_grad", L.moe_router_adapters_grad(
+        ph, px, dt, pw, pa, pb, pi, ps, pu, m, d, n, r, na, None if dx is None else dx.data_ptr(), da.data_ptr(),
+        db.data_ptr(), None if dw_r is None else dw_r.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _raw_stream(dev)))
     return dx, da, db, dw_r
 
 
-def _loss_shapes(logits, topk_idx, seq_offsets, token_mask):
+def _loss_args(logits, topk_idx, seq_offsets, token_mask):
     m, n = logits.shape
     k = topk_idx.shape[1]
     nseq = seq_offsets.shape[0] - 1
-    dev = logits.device
-    _need_on(dev, logits, torch.float32, (m, n), "logits")
-    _need_on(dev, topk_idx, torch.int32, (m, k), "topk_idx")
-    _need_on(dev, seq_offsets, torch.int32, (nseq + 1,), "seq_offsets")
-    if token_mask is not None:
-        _need_on(dev, token_mask, torch.uint8, (m,), "token_mask")
-    return m, n, k, nseq, dev
+    dev = logits.get_device()
+    return dev, (m, n, k, nseq), (
+        _chk(dev, logits, torch.float32, (m, n), "logits"), _chk(dev, topk_idx, torch.int32, (m, k), "topk_idx"),
+        _chk(dev, seq_offsets, torch.int32, (nseq + 1,), "seq_offsets"),
+        None if token_mask is None else _chk(dev, token_mask, torch.uint8, (m,), "token_mask"))
 
 
+@_on_stream
 def moe_router_loss(logits, topk_idx, seq_offsets, token_mask=None, score_fn=MOE_SOFTMAX, alpha=1e-2, alpha_seq=0.0,
-                    z_coef=0.0, out=None, workspace=None, stream=None):
+                    z_coef=0.0, out=None, workspace=None):
     """Balance loss of the counted tokens of a ragged batch, its sequence-wise mean and the z-loss. Returns
     dict(loss [4] (total, batch, sequences, z), counts [nseq+1, n] int32, tokens [nseq+1] int32, f, P [nseq+1, n]);
-    row nseq is the whole batch."""
-    m, n, k, nseq, dev = _loss_shapes(logits, topk_idx, seq_offsets, token_mask)
-    with _on(dev, stream):
-        out = dict() if out is None else out
-        res = dict(loss=_out(dev, out.get("loss"), torch.float32, (4,), "loss"),
-                   counts=_out(dev, out.get("counts"), torch.int32, (nseq + 1, n), "counts"),
-                   tokens=_out(dev, out.get("tokens"), torch.int32, (nseq + 1,), "tokens"),
-                   f=_out(dev, out.get("f"), torch.float32, (nseq + 1, n), "f"),
-                   P=_out(dev, out.get("P"), torch.float32, (nseq + 1, n), "P"))
-        workspace = _work_on(dev, workspace, lib().moe_router_loss_workspace_size(m, n, nseq))
-        _check("moe_router_loss", lib().moe_router_loss(
-            _ptr(logits), _ptr(topk_idx), m, n, k, _ptr(seq_offsets), nseq, _ptr(token_mask), score_fn, alpha,
-            alpha_seq, z_coef, _ptr(res["loss"]), _ptr(res["counts"]), _ptr(res["tokens"]), _ptr(res["f"]),
-            _ptr(res["P"]), _ptr(workspace), workspace.numel(), _stream(stream)))
+    row nseq is the whole batch. `out`: such a dict to fill (its missing tensors are made)."""
+    dev, (m, n, k, nseq), (pl, pi, po, pm) = _loss_args(logits, topk_idx, seq_offsets, token_mask)
+    L = lib()
+    out = {} if out is None else out
+    f32, i32 = torch.float32, torch.int32
+    res = dict(loss=_out(dev, out.get("loss"), f32, (4,), "loss"),
+               counts=_out(dev, out.get("counts"), i32, (nseq + 1, n), "counts"),
+               tokens=_out(dev, out.get("tokens"), i32, (nseq + 1,), "tokens"),
+               f=_out(dev, out.get("f"), f32, (nseq + 1, n), "f"), P=_out(dev, out.get("P"), f32, (nseq + 1, n), "P"))
+    workspace = _work(dev, workspace, L.moe_router_loss_workspace_size, m, n, nseq)
+    _check("moe_router_loss", L.moe_router_loss(
+        pl, pi, m, n, k, po, nseq, pm, score_fn, alpha, alpha_seq, z_coef, res["loss"].data_ptr(),
+        res["counts"].data_ptr(), res["tokens"].data_ptr(), res["f"].data_ptr(), res["P"].data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(dev)))
     return res
 
 
+@_on_stream
 def moe_router_loss_grad(logits, topk_idx, seq_offsets, counts, tokens, token_mask=None, score_fn=MOE_SOFTMAX,
-                         alpha=1e-2, alpha_seq=0.0, z_coef=0.0, dloss=None, dgate=None, renorm_topk=0, dlogits=None,
-                         stream=None):
+                         alpha=1e-2, alpha_seq=0.0, z_coef=0.0, dloss=None, dgate=None, renorm_topk=0, dlogits=None):
     """Gradient of moe_router_loss's total (times the device scalar dloss [1], 1 without it) and of the gates
     (dgate [m, k]) with respect to the logits. Returns dlogits [m, n]; padding and masked rows are 0."""
-    m, n, k, nseq, dev = _loss_shapes(logits, topk_idx, seq_offsets, token_mask)
-    _need_on(dev, counts, torch.int32, (nseq + 1, n), "counts")
-    _need_on(dev, tokens, torch.int32, (nseq + 1,), "tokens")
-    if dloss is not None:
-        _need_on(dev, dloss, torch.float32, (1,), "dloss")
-    if dgate is not None:
-        _need_on(dev, dgate, torch.float32, (m, k), "dgate")
-    with _on(dev, stream):
-        dlogits = _out(dev, dlogits, torch.float32, (m, n), "dlogits")
-        _check("moe_router_loss_grad", lib().moe_router_loss_grad(
-            _ptr(logits), _ptr(topk_idx), m, n, k, _ptr(seq_offsets), nseq, _ptr(token_mask), score_fn, alpha,
-            alpha_seq, z_coef, _ptr(counts), _ptr(tokens), _ptr(dloss), _ptr(dgate), renorm_topk, _ptr(dlogits),
-            _stream(stream)))
+    dev, (m, n, k, nseq), (pl, pi, po, pm) = _loss_args(logits, topk_idx, seq_offsets, token_mask)
+    f32, i32 = torch.float32, torch.int32
+    pc, pt = _chk(dev, counts, i32, (nseq + 1, n), "counts"), _chk(dev, tokens, i32, (nseq + 1,), "tokens")
+    pd = None if dloss is None else _chk(dev, dloss, f32, (1,), "dloss")
+    pg = None if dgate is None else _chk(dev, dgate, f32, (m, k), "dgate")
+    dlogits = _out(dev, dlogits, f32, (m, n), "dlogits")
+    _check("moe_router_loss_grad", lib().moe_router_loss_grad(
+        pl, pi, m, n, k, po, nseq, pm, score_fn, alpha, alpha_seq, z_coef, pc, pt, pd, pg, renorm_topk,
+        dlogits.data_ptr(), _raw_stream(dev)))
     return dlogits
 
 
-def moe_combine_grad(dy, ybuf, dest_row, topk_gate, dybuf=None, dgate=None, want_dybuf=True, stream=None):
+@_on_stream
+def moe_combine_grad(dy, ybuf, dest_row, topk_gate, dybuf=None, dgate=None, want_dybuf=True):
     """Backward of moe_combine: (dybuf [max_rows, d] with dybuf[dest_row[i, r]] = g_ir dy_i or None,
     dgate [m, k] fp32 = <dy_i, ybuf[dest_row[i, r]]>, 0 for dropped picks). A dybuf made here is zero in the rows
     that no pick names; a given one keeps them as they were."""
     m, d = dy.shape
     k = dest_row.shape[1]
     max_rows = ybuf.shape[0]
-    dev = dy.device
-    dt = _dtype_code(dy)
-    _need_on(dev, dy, dy.dtype, (m, d), "dy")
-    _need_on(dev, ybuf, dy.dtype, (max_rows, d), "ybuf")
-    _need_on(dev, dest_row, torch.int32, (m, k), "dest_row")
-    _need_on(dev, topk_gate, torch.float32, (m, k), "topk_gate")
-    with _on(dev, stream):
-        if dybuf is None and want_dybuf:
-            dybuf = torch.zeros((max_rows, d), dtype=dy.dtype, device=dev)
-        if dybuf is not None:
-            _need_on(dev, dybuf, dy.dtype, (max_rows, d), "dybuf")
-        dgate = _out(dev, dgate, torch.float32, (m, k), "dgate")
-        _check("moe_combine_grad", lib().moe_combine_grad(
-            _ptr(dy), _ptr(ybuf), dt, _ptr(dest_row), _ptr(topk_gate), m, k, d, max_rows, _ptr(dybuf), _ptr(dgate),
-            _stream(stream)))
+    dev, dt = dy.get_device(), dy.dtype
+    py, pb = _chk(dev, dy, dt, (m, d), "dy"), _chk(dev, ybuf, dt, (max_rows, d), "ybuf")
+    pr, pg = _chk(dev, dest_row, torch.int32, (m, k), "dest_row"), _chk(dev, topk_gate, torch.float32, (m, k), "topk_gate")
+    if dybuf is None and want_dybuf:
+        dybuf = torch.zeros((max_rows, d), dtype=dt, device=dy.device)
+    po = None if dybuf is None else _chk(dev, dybuf, dt, (max_rows, d), "dybuf")
+    dgate = _out(dev, dgate, torch.float32, (m, k), "dgate")
+    _check("moe_combine_grad", lib().moe_combine_grad(
+        py, pb, _torch_dtype_code(dt), pr, pg, m, k, d, max_rows, po, dgate.data_ptr(), _raw_stream(dev)))
     return dybuf, dgate

@@ -8,16 +8,19 @@
 // Backward, dh = dL/dh:
 //   du_i = s_a B_a^T dh_i,  dx_i = W_r dh_i + A_a^T du_i,
 //   dA_a = sum_{i in a} du_i x_i^T,  dB_a = s_a sum_{i in a} dh_i u_i^T,  dW_r = sum_i x_i dh_i^T.
-#include "common.cuh"
+#include <atomic>
+
+#include "tc_ptx.cuh"
 
 namespace moe {
 
 namespace adp {
 constexpr int kThreads = 256;
 constexpr int kPad = 64;        // a group's rows are padded to this many in the grouped order
-constexpr int kSeg = 512;       // rows of one partial sum of the row contractions
 constexpr int kTile = 256;      // rows of a tensor-core row tile
 constexpr int kPlanThreads = 1024;
+constexpr int kCluster = 8;     // CTAs that group the rows of a large batch
+constexpr int kClusterRows = 2048;  // above this many rows (one CTA: 6 us for 8191 rows, 62 us for 65536)
 }  // namespace adp
 
 // Rows grouped by adapter (group na: rows without one), in row order inside a group, each group
@@ -26,12 +29,10 @@ struct AdapterPlan {
     int32_t *perm;   // [m_pad] row of each grouped position, or -1
     int32_t *goff;   // [na + 2] first grouped position of each group
     int32_t *gcnt;   // [na + 1] rows of each group
-    int32_t *sseg;   // [na + 2] first segment (kSeg grouped positions) of each group
     int32_t *tstart; // [na + 2] first row tile (kTile grouped positions) of each group
 };
 
 static int64_t adapter_padded_rows(int64_t m, int na) { return m + (int64_t)adp::kPad * (na + 1); }
-static int64_t adapter_segments(int64_t rows, int groups) { return (rows + adp::kSeg - 1) / adp::kSeg + groups; }
 
 static size_t adapter_plan_layout(int64_t m, int na, AdapterPlan* plan, char* base) {
     size_t off = 0;
@@ -40,150 +41,212 @@ static size_t adapter_plan_layout(int64_t m, int na, AdapterPlan* plan, char* ba
     p = take((size_t)adapter_padded_rows(m, na)); if (plan) plan->perm = p;
     p = take((size_t)na + 2);                     if (plan) plan->goff = p;
     p = take((size_t)na + 1);                     if (plan) plan->gcnt = p;
-    p = take((size_t)na + 2);                     if (plan) plan->sseg = p;
     p = take((size_t)na + 2);                     if (plan) plan->tstart = p;
     return off;
 }
 
-struct AdapterWs {
-    AdapterPlan plan;
-    float *du;       // [m, r]
-    float *part;     // [segments, q, p] partial sums of the row contractions
-};
-
-static size_t adapter_ws_layout(int64_t m, int d, int n, int r, int na, AdapterWs* w, char* base) {
-    size_t off = adapter_plan_layout(m, na, w ? &w->plan : nullptr, base);
-    auto take = [&](size_t bytes) { char* p = base + off; off += (bytes + 255) & ~size_t(255); return p; };
-    char* p;
-    const int64_t mp = adapter_padded_rows(m, na);
-    p = take(4 * (size_t)m * r);       if (w) w->du = (float*)p;
-    const size_t by_group = (size_t)adapter_segments(mp, na + 1) * r * (size_t)(d > n ? d : n);
-    const size_t all = (size_t)adapter_segments(m, 1) * d * n;
-    p = take(4 * (by_group > all ? by_group : all)); if (w) w->part = (float*)p;
-    return off;
+// Largest g in [0, groups) with start[g] <= t.
+__device__ __forceinline__ int group_at(const int32_t* __restrict__ start, int groups, int t) {
+    int lo = 0, hi = groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= t) lo = mid; else hi = mid;
+    }
+    return lo;
 }
 
-// Stable grouping of the rows by adapter in one CTA (block 0). Warp w takes a run of consecutive rows; a
-// histogram per warp, their scan over (group, warp), then each warp places its rows: within 32 rows
-// the lanes of one group rank themselves by a match. Block 0 also clears the tickets.
-// The other blocks, where the tensor cores need it, write W_r [d, n] fp32 in bf16 parts that add up to it:
-// three parts as wparts [3, n, d] (transposed, for x W_r), or two as wparts [2, d, nk], nk >= n with zeros
-// behind n (for dh W_r^T).
+// What the blocks behind the plan's do: parts of W_r for the tensor cores, or du for the fp32 kernels.
+struct PrepExtra {
+    const float* w_r;       // W_r [d, n] ...
+    int d, n, nk, parts;    // ... as bf16 parts that add up to it: three as [3, n, d] (transposed, for x W_r), or two
+    __nv_bfloat16* wparts;  // as [2, d, nk], nk >= n with zeros behind n (for dh W_r^T)
+    const float *dh, *b, *scale;  // du_ij = s_a sum_e dh_ie B_a[e, j], a warp per row, lanes along j
+    int r;
+    float* du;
+};
+
+// Stable grouping of the rows by adapter by one cluster (blocks 0 .. its size - 1). Each warp takes a run of
+// consecutive rows: a histogram per warp, sums over the warps and the CTAs before, then each warp places its rows;
+// within 32 rows the lanes of one group rank themselves by a match. Block 0 also clears the tickets.
 __global__ void __launch_bounds__(adp::kPlanThreads)
 adapter_prep_kernel(const int32_t* __restrict__ idx, int64_t m, int na, AdapterPlan p, int32_t* __restrict__ tickets,
-                    int64_t ntickets, const float* __restrict__ w_r, int d, int n, int nk, int parts,
-                    __nv_bfloat16* __restrict__ wparts) {
+                    int64_t ntickets, PrepExtra x, int cluster) {
     using namespace adp;
-    extern __shared__ int hist[];  // [32][na + 1]
+    extern __shared__ int hist[];  // [32][G] per warp; [G] this CTA's counts; [G] all counts; [G] first position
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, G = na + 1;
     pdl_trigger();
     pdl_wait();
-    if (blockIdx.x > 0) {
+    if ((int)blockIdx.x >= cluster) {
+        const int b = (int)blockIdx.x - cluster;
+        if (x.du) {
+            const int64_t row = (int64_t)b * 32 + wid;
+            if (row >= m) return;
+            const int ad = idx[row];
+            const bool has = ad >= 0 && ad < na;
+            for (int j = lane; j < x.r; j += 32) {
+                float t = 0.f;
+                if (has) {
+                    const float* bp = x.b + (int64_t)ad * x.n * x.r + j;
+#pragma unroll 8
+                    for (int e = 0; e < x.n; ++e) t = fmaf(x.dh[row * x.n + e], bp[(int64_t)e * x.r], t);
+                    t *= x.scale[ad];
+                }
+                x.du[row * x.r + j] = t;
+            }
+            return;
+        }
         __shared__ float tile[32][33];
-        const int nb = (n + 31) / 32, b = (int)blockIdx.x - 1;
+        const int d = x.d, n = x.n, nb = (n + 31) / 32;
         const int t0 = b / nb * 32, j0 = b % nb * 32;
-        float v = (t0 + wid < d && j0 + lane < n) ? w_r[(int64_t)(t0 + wid) * n + j0 + lane] : 0.f;
+        if (t0 >= d) return;
+        float v = (t0 + wid < d && j0 + lane < n) ? x.w_r[(int64_t)(t0 + wid) * n + j0 + lane] : 0.f;
         int j = j0 + lane, t = t0 + wid;
-        if (parts == 3) {
+        if (x.parts == 3) {
             tile[wid][lane] = v;
             __syncthreads();
             j = j0 + wid;
             t = t0 + lane;
             v = tile[lane][wid];
         }
-        if (j >= (parts == 3 ? n : nk) || t >= d) return;
+        if (j >= (x.parts == 3 ? n : x.nk) || t >= d) return;
         const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
         const float r1 = v - __bfloat162float(p0);
         const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
-        const int64_t o = parts == 3 ? (int64_t)j * d + t : (int64_t)t * nk + j;
-        const int64_t plane = parts == 3 ? (int64_t)n * d : (int64_t)d * nk;
-        wparts[o] = p0;
-        wparts[plane + o] = p1;
-        if (parts == 3) wparts[2 * plane + o] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
+        const int64_t o = x.parts == 3 ? (int64_t)j * d + t : (int64_t)t * x.nk + j;
+        const int64_t plane = x.parts == 3 ? (int64_t)n * d : (int64_t)d * x.nk;
+        x.wparts[o] = p0;
+        x.wparts[plane + o] = p1;
+        if (x.parts == 3) x.wparts[2 * plane + o] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
         return;
     }
-    for (int64_t i = tid; i < ntickets; i += kPlanThreads) tickets[i] = 0;
+    int* own = hist + 32 * G;
+    int* all = own + G;
+    int* first = all + G;
+    const int rank = blockIdx.x;
+    for (int64_t i = (int64_t)rank * kPlanThreads + tid; i < ntickets; i += (int64_t)cluster * kPlanThreads) tickets[i] = 0;
     for (int i = tid; i < 32 * G; i += kPlanThreads) hist[i] = 0;
     __syncthreads();
-    const int64_t per = ((m + 31) / 32 + 31) / 32 * 32;  // rows per warp, a multiple of 32
-    const int64_t r0 = min(wid * per, m), r1 = min(r0 + per, m);
-    for (int64_t b = r0; b < r1; b += 32) {
-        const int64_t r = b + lane;
-        int g = -1;
-        if (r < r1) {
-            g = idx[r];
-            if (g < -1 || g >= na) record_error(kErrAdapterIndex);
-            if (g < 0 || g >= na) g = na;
+    const int64_t warps = 32 * cluster, per = ((m + warps - 1) / warps + 31) / 32 * 32;  // rows per warp, a multiple of 32
+    const int64_t r0 = min((rank * 32 + wid) * per, m), r1 = min(r0 + per, m);
+    int* mine = hist + wid * G;
+    for (int64_t b = r0; b < r1; b += 128) {
+        int g[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) g[q] = b + 32 * q + lane < r1 ? idx[b + 32 * q + lane] : -2;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const bool in = b + 32 * q + lane < r1;
+            if (in && (g[q] < -1 || g[q] >= na)) record_error(kErrAdapterIndex);
+            const int v = !in ? -1 : (g[q] < 0 || g[q] >= na ? na : g[q]);
+            const unsigned same = __match_any_sync(0xffffffffu, v);
+            if (v >= 0 && lane == __ffs(same) - 1) mine[v] += __popc(same);
+            __syncwarp();
         }
-        const unsigned same = __match_any_sync(0xffffffffu, g);
-        if (g >= 0 && lane == __ffs(same) - 1) hist[wid * G + g] += __popc(same);
-        __syncwarp();
     }
     __syncthreads();
-    // group totals, then offsets by one warp
     for (int g = tid; g < G; g += kPlanThreads) {
         int c = 0;
         for (int w = 0; w < 32; ++w) c += hist[w * G + g];
-        p.gcnt[g] = c;
+        own[g] = c;
+    }
+    if (cluster > 1) ptx::cluster_sync(); else __syncthreads();
+    for (int g = tid; g < G; g += kPlanThreads) {
+        int sum = 0, before = 0;
+        for (int k = 0; k < cluster; ++k) {
+            const int c = cluster > 1 ? ptx::ld_cluster_s32(ptx::mapa_shared(ptx::smem_u32(own + g), k)) : own[g];
+            sum += c;
+            if (k < rank) before += c;
+        }
+        all[g] = sum;
+        first[g] = before;
     }
     __syncthreads();
     if (wid == 0) {
-        int base = 0, seg = 0, til = 0;
+        int base = 0, til = 0;
         for (int g0 = 0; g0 < G; g0 += 32) {
             const int g = g0 + lane;
-            const int c = g < G ? p.gcnt[g] : 0;
-            const int pc = (c + kPad - 1) / kPad * kPad, sc = (pc + kSeg - 1) / kSeg, tc = (pc + kTile - 1) / kTile;
-            int a = pc, s = sc, t = tc;
+            const int c = g < G ? all[g] : 0;
+            const int pc = (c + kPad - 1) / kPad * kPad, tc = (pc + kTile - 1) / kTile;
+            int a = pc, t = tc;
             for (int o = 1; o < 32; o <<= 1) {
-                const int ua = __shfl_up_sync(0xffffffffu, a, o), us = __shfl_up_sync(0xffffffffu, s, o);
-                const int ut = __shfl_up_sync(0xffffffffu, t, o);
-                if (lane >= o) { a += ua; s += us; t += ut; }
+                const int ua = __shfl_up_sync(0xffffffffu, a, o), ut = __shfl_up_sync(0xffffffffu, t, o);
+                if (lane >= o) { a += ua; t += ut; }
             }
-            if (g < G) { p.goff[g] = base + a - pc; p.sseg[g] = seg + s - sc; p.tstart[g] = til + t - tc; }
+            if (g < G) {
+                first[g] += base + a - pc;
+                if (rank == 0) { p.goff[g] = base + a - pc; p.gcnt[g] = c; p.tstart[g] = til + t - tc; }
+            }
             base += __shfl_sync(0xffffffffu, a, 31);
-            seg += __shfl_sync(0xffffffffu, s, 31);
             til += __shfl_sync(0xffffffffu, t, 31);
         }
-        if (lane == 0) { p.goff[G] = base; p.sseg[G] = seg; p.tstart[G] = til; }
+        if (rank == 0 && lane == 0) { p.goff[G] = base; p.tstart[G] = til; }
     }
     __syncthreads();
     for (int g = tid; g < G; g += kPlanThreads) {
-        int at = p.goff[g];
+        int at = first[g];
         for (int w = 0; w < 32; ++w) { const int c = hist[w * G + g]; hist[w * G + g] = at; at += c; }
-        for (; at < p.goff[g + 1]; ++at) p.perm[at] = -1;
+        if (rank == cluster - 1)  // behind the group's last row
+            for (int q = all[g]; q % kPad != 0; ++q) p.perm[at++] = -1;
     }
     __syncthreads();
-    for (int64_t b = r0; b < r1; b += 32) {
-        const int64_t r = b + lane;
-        int g = -1;
-        if (r < r1) {
-            g = idx[r];
-            if (g < 0 || g >= na) g = na;
+    for (int64_t b = r0; b < r1; b += 128) {
+        int g[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) g[q] = b + 32 * q + lane < r1 ? idx[b + 32 * q + lane] : -2;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int64_t r = b + 32 * q + lane;
+            const int v = r >= r1 ? -1 : (g[q] < 0 || g[q] >= na ? na : g[q]);
+            const unsigned same = __match_any_sync(0xffffffffu, v);
+            const int place = __popc(same & ((1u << lane) - 1u));
+            const int at = v >= 0 ? mine[v] : 0;
+            __syncwarp();
+            if (v >= 0) {
+                p.perm[at + place] = (int32_t)r;
+                if (place == 0) mine[v] = at + __popc(same);
+            }
+            __syncwarp();
         }
-        const unsigned same = __match_any_sync(0xffffffffu, g);
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        const int at = g >= 0 ? hist[wid * G + g] : 0;
-        __syncwarp();
-        if (g >= 0) {
-            p.perm[at + rank] = (int32_t)r;
-            if (rank == 0) hist[wid * G + g] = at + __popc(same);
-        }
-        __syncwarp();
     }
+    if (cluster > 1) ptx::cluster_sync();  // nobody leaves while its counts may still be read
 }
 
-// wparts == NULL: the plan alone.
+// Set a kernel's shared-memory limit, once per device (the attribute belongs to the device).
+template <auto Kernel>
+static cudaError_t need_smem(size_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1u))) return e;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    return e;
+}
+
 static cudaError_t launch_adapter_prep(const int32_t* idx, int64_t m, int na, const AdapterPlan& p, int32_t* tickets,
-                                       int64_t ntickets, const float* w_r, int d, int n, int nk, int parts,
-                                       __nv_bfloat16* wparts, cudaStream_t stream) {
-    const size_t smem = sizeof(int) * 32 * (size_t)(na + 1);
-    // set on every call: the attribute belongs to the current device
-    cudaError_t e = cudaFuncSetAttribute(adapter_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(sizeof(int) * 32 * (kMaxAdapters + 1)));
+                                       int64_t ntickets, const PrepExtra& x, cudaStream_t stream) {
+    const size_t per = sizeof(int) * 35;  // bytes per group
+    const cudaError_t e = need_smem<adapter_prep_kernel>(per * (kMaxAdapters + 1));
     if (e != cudaSuccess) return e;
-    const unsigned blocks = 1 + (wparts ? (unsigned)((d + 31) / 32) * (unsigned)((n + 31) / 32) : 0);
-    return launch_pdl(adapter_prep_kernel, dim3(blocks), dim3(adp::kPlanThreads), smem, stream, idx, m, na, p, tickets,
-                      ntickets, w_r, d, n, nk, parts, wparts);
+    const int cluster = m > adp::kClusterRows ? adp::kCluster : 1;
+    int64_t extra = 0;
+    if (x.wparts) extra = (int64_t)((x.d + 31) / 32) * ((x.n + 31) / 32);
+    if (x.du) extra = (m + 31) / 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(cluster + (extra + cluster - 1) / cluster * cluster));
+    cfg.blockDim = dim3(adp::kPlanThreads);
+    cfg.dynamicSmemBytes = per * (size_t)(na + 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, adapter_prep_kernel, idx, m, na, p, tickets, ntickets, x, cluster);
 }
 
 // ---- forward: R rows per CTA, thread (column, row group); 32 input columns at a time through
@@ -286,28 +349,6 @@ adapters_rows_kernel(const float* __restrict__ x, const float* __restrict__ w_r,
     }
 }
 
-// ---- du_ij = s_a sum_e dh_ie B_a[e, j]: a warp per row, lanes along j
-__global__ void __launch_bounds__(adp::kThreads)
-adapters_du_kernel(const float* __restrict__ dh, const float* __restrict__ bmat, const int32_t* __restrict__ idx,
-                   const float* __restrict__ scale, int64_t m, int n, int r, int na, float* __restrict__ du) {
-    const int lane = threadIdx.x & 31;
-    pdl_trigger();
-    pdl_wait();
-    const int64_t row = (int64_t)blockIdx.x * (adp::kThreads / 32) + (threadIdx.x >> 5);
-    if (row >= m) return;
-    const int ad = idx[row];
-    const bool has = ad >= 0 && ad < na;
-    for (int j = lane; j < r; j += 32) {
-        float t = 0.f;
-        if (has) {
-            const float* bp = bmat + (int64_t)ad * n * r + j;
-            for (int e = 0; e < n; ++e) t = fmaf(dh[row * n + e], bp[(int64_t)e * r], t);
-            t *= scale[ad];
-        }
-        du[row * r + j] = t;
-    }
-}
-
 // ---- dx: 16 rows x 128 columns of d per CTA
 __global__ void __launch_bounds__(adp::kThreads)
 adapters_dx_kernel(const float* __restrict__ dh, const float* __restrict__ w_r, const float* __restrict__ a,
@@ -363,66 +404,91 @@ adapters_dx_kernel(const float* __restrict__ dh, const float* __restrict__ w_r, 
     }
 }
 
-// ---- row contractions: part[seg][q][p] = sum over the segment's rows of X[row][p] Y[row][q].
-// 64 x 64 tiles, 4 x 4 per thread, 16 rows at a time (summed first, then added). perm == NULL: the
-// rows in order, one group.
+// ---- row contractions out[g][q][p] = s_g sum over the rows of group g of X[row][p] Y[row][q].
+// A segment is what a window of `seg` grouped positions has of one group: window w and group g give segment w + g
+// (unique: each next segment advances the window or the group). Its partial sums are left as part[segment][q][p] and
+// folded in order.
+struct RowsTask {
+    const float *X, *Y, *scale;
+    int np, nq, seg, grouped;  // grouped 0: the rows in order, one group
+    int ptiles, qtiles;
+    int64_t segs;
+    float *part, *out;
+};
+struct RowsTasks {
+    RowsTask t[3];
+    int count;
+};
+
+// 64 x 64 tiles, 4 x 4 per thread, 64 rows at a time; 16 rows' products are summed first and then added.
 __global__ void __launch_bounds__(adp::kThreads)
-rows_outer_kernel(const float* __restrict__ X, int np, const float* __restrict__ Y, int nq, int64_t m, int groups,
-                  AdapterPlan plan, float* __restrict__ part) {
+rows_outer_kernel(RowsTasks tasks, int64_t m, int groups, AdapterPlan plan) {
     using namespace adp;
-    constexpr int RB = 16;
+    constexpr int RB = 64;
     __shared__ float xs[RB][65], ys[RB][65];
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, c = tid & 63;
     pdl_trigger();
     pdl_wait();
-    const int seg = blockIdx.z;
-    int64_t b = (int64_t)seg * kSeg, end = min(b + kSeg, m);
-    if (plan.perm) {
-        if (seg >= plan.sseg[groups]) return;
-        int lo = 0, hi = groups;  // largest group with sseg <= seg
+    int64_t blk = blockIdx.x;
+    int ti = 0;
+    while (ti + 1 < tasks.count && blk >= (int64_t)tasks.t[ti].ptiles * tasks.t[ti].qtiles * tasks.t[ti].segs) {
+        blk -= (int64_t)tasks.t[ti].ptiles * tasks.t[ti].qtiles * tasks.t[ti].segs;
+        ++ti;
+    }
+    const RowsTask& T = tasks.t[ti];
+    const int p0 = (int)(blk % T.ptiles) * 64, q0 = (int)(blk / T.ptiles % T.qtiles) * 64;
+    const int64_t seg = blk / ((int64_t)T.ptiles * T.qtiles);
+    int64_t b = seg * T.seg, end = min(b + T.seg, m);
+    if (T.grouped) {
+        int lo = 0, hi = groups;  // largest group whose first segment is <= seg
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (plan.sseg[mid] <= seg) lo = mid; else hi = mid;
+            if (plan.goff[mid] / T.seg + mid <= seg) lo = mid; else hi = mid;
         }
-        b = plan.goff[lo] + (int64_t)(seg - plan.sseg[lo]) * kSeg;
-        end = min(b + kSeg, (int64_t)plan.goff[lo + 1]);
-    } else if (b >= m) {
-        return;
+        const int64_t w = seg - lo;
+        b = max(w * T.seg, (int64_t)plan.goff[lo]);
+        end = min((w + 1) * T.seg, (int64_t)plan.goff[lo + 1]);
     }
-    const int p0 = blockIdx.x * 64, q0 = blockIdx.y * 64;
+    if (b >= end) return;
     float acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
     for (int64_t at = b; at < end; at += RB) {
-        for (int i = tid; i < RB * 64; i += kThreads) {
-            const int rr = i >> 6, c = i & 63;
-            int64_t row = -1;
-            if (at + rr < end) row = plan.perm ? plan.perm[at + rr] : at + rr;
-            xs[rr][c] = (row >= 0 && p0 + c < np) ? X[row * np + p0 + c] : 0.f;
-            ys[rr][c] = (row >= 0 && q0 + c < nq) ? Y[row * nq + q0 + c] : 0.f;
+        int32_t row[RB / 4];
+#pragma unroll
+        for (int i = 0; i < RB / 4; ++i) {
+            const int64_t q = at + (tid >> 6) + 4 * i;
+            row[i] = q < end ? (T.grouped ? plan.perm[q] : (int32_t)q) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < RB / 4; ++i) {
+            xs[(tid >> 6) + 4 * i][c] = (row[i] >= 0 && p0 + c < T.np) ? T.X[(int64_t)row[i] * T.np + p0 + c] : 0.f;
+            ys[(tid >> 6) + 4 * i][c] = (row[i] >= 0 && q0 + c < T.nq) ? T.Y[(int64_t)row[i] * T.nq + q0 + c] : 0.f;
         }
         __syncthreads();
-        float blk[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) blk[i][j] = 0.f;
-#pragma unroll
-        for (int rr = 0; rr < RB; ++rr) {
-            float xv[4], yv[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { xv[i] = xs[rr][tx + 16 * i]; yv[i] = ys[rr][ty + 16 * i]; }
+        for (int r0 = 0; r0 < RB; r0 += 16) {
+            float blk4[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) blk[i][j] = fmaf(xv[j], yv[i], blk[i][j]);
+                for (int j = 0; j < 4; ++j) blk4[i][j] = 0.f;
+#pragma unroll
+            for (int rr = 0; rr < 16; ++rr) {
+                float xv[4], yv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) { xv[i] = xs[r0 + rr][tx + 16 * i]; yv[i] = ys[r0 + rr][ty + 16 * i]; }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) blk4[i][j] = fmaf(xv[j], yv[i], blk4[i][j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] += blk4[i][j];
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] += blk[i][j];
         __syncthreads();
     }
 #pragma unroll
@@ -430,39 +496,73 @@ rows_outer_kernel(const float* __restrict__ X, int np, const float* __restrict__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int p = p0 + tx + 16 * j, q = q0 + ty + 16 * i;
-            if (p < np && q < nq) part[((int64_t)seg * nq + q) * np + p] = acc[i][j];
+            if (p < T.np && q < T.nq) T.part[(seg * T.nq + q) * T.np + p] = acc[i][j];
         }
 }
 
-// out[g][i] = s_g * sum over the group's segments, in order, of part[seg][i] (zero for no rows)
+// out[g][i] = s_g * sum over the group's segments, in order, of part[segment][i] (zero for no rows).
+// blockIdx.y = group; blockIdx.x runs over the tasks' outputs.
 __global__ void __launch_bounds__(adp::kThreads)
-rows_fold_kernel(const float* __restrict__ part, int64_t per, int64_t segs, AdapterPlan plan,
-                 const float* __restrict__ scale, float* __restrict__ out) {
+rows_fold_kernel(RowsTasks tasks, AdapterPlan plan) {
     pdl_trigger();
     pdl_wait();
     const int g = blockIdx.y;
-    const int64_t i = (int64_t)blockIdx.x * adp::kThreads + threadIdx.x;
-    if (i >= per) return;
-    const int64_t s0 = plan.perm ? plan.sseg[g] : 0, s1 = plan.perm ? plan.sseg[g + 1] : segs;
+    int64_t blk = blockIdx.x;
+    int ti = 0;
+    while (ti + 1 < tasks.count) {
+        const int64_t mine = ((int64_t)tasks.t[ti].np * tasks.t[ti].nq + adp::kThreads - 1) / adp::kThreads;
+        if (blk < mine) break;
+        blk -= mine;
+        ++ti;
+    }
+    const RowsTask& T = tasks.t[ti];
+    const int64_t per = (int64_t)T.np * T.nq, i = blk * adp::kThreads + threadIdx.x;
+    if (i >= per || (!T.grouped && g > 0)) return;
+    int64_t s0 = 0, s1 = T.segs;
+    if (T.grouped) {
+        const int o0 = plan.goff[g], o1 = plan.goff[g + 1];
+        s0 = o0 / T.seg + g;
+        s1 = o1 > o0 ? (o1 - 1) / T.seg + g + 1 : s0;
+    }
     float t = 0.f;
-    for (int64_t s = s0; s < s1; ++s) t += part[s * per + i];
-    out[g * per + i] = scale ? scale[g] * t : t;
+#pragma unroll 4
+    for (int64_t s = s0; s < s1; ++s) t += T.part[s * per + i];
+    T.out[g * per + i] = T.scale ? T.scale[g] * t : t;
 }
 
-static cudaError_t launch_rows_contract(const float* X, int np, const float* Y, int nq, int64_t m, int na,
-                                        const AdapterPlan& plan, const float* scale, float* part, float* out,
-                                        cudaStream_t stream) {
-    const bool grouped = plan.perm != nullptr;
-    const int64_t segs = grouped ? adapter_segments(adapter_padded_rows(m, na), na + 1)
-                                 : (m + adp::kSeg - 1) / adp::kSeg;
-    cudaError_t e = cudaSuccess;
-    if (segs > 0)
-        e = launch_pdl(rows_outer_kernel, dim3((unsigned)((np + 63) / 64), (unsigned)((nq + 63) / 64), (unsigned)segs),
-                       dim3(adp::kThreads), 0, stream, X, np, Y, nq, m, na + 1, plan, part);
-    if (e != cudaSuccess) return e;
-    const int64_t per = (int64_t)np * nq;
-    return launch_pdl(rows_fold_kernel, dim3((unsigned)((per + adp::kThreads - 1) / adp::kThreads), grouped ? na : 1),
-                      dim3(adp::kThreads), 0, stream, part, per, segs, plan, scale, out);
+// A task over `rows` (grouped: padded) rows. Segments of 64 rows, longer where their partial sums would take more
+// than 16 MB.
+static RowsTask rows_task(const float* X, int np, const float* Y, int nq, int64_t rows, int groups, bool grouped) {
+    RowsTask t = {};
+    t.X = X; t.Y = Y; t.np = np; t.nq = nq; t.grouped = grouped ? 1 : 0;
+    t.ptiles = (np + 63) / 64;
+    t.qtiles = (nq + 63) / 64;
+    t.seg = 64;
+    while ((int64_t)t.seg < rows && (rows / t.seg) * np * nq * 4 > ((int64_t)16 << 20)) t.seg *= 2;
+    t.segs = (rows + t.seg - 1) / t.seg + (grouped ? groups : 0);
+    return t;
+}
+
+struct AdapterWs {
+    AdapterPlan plan;
+    float* du;       // [m, r]
+    RowsTask task[3];  // dA, dB, dW_r
+};
+
+static size_t adapter_ws_layout(int64_t m, int d, int n, int r, int na, AdapterWs* w, char* base) {
+    size_t off = adapter_plan_layout(m, na, w ? &w->plan : nullptr, base);
+    auto take = [&](size_t bytes) { char* p = base + off; off += (bytes + 255) & ~size_t(255); return p; };
+    char* p;
+    p = take(4 * (size_t)m * r);       if (w) w->du = (float*)p;
+    const int64_t mp = adapter_padded_rows(m, na);
+    RowsTask t[3] = {rows_task(nullptr, d, nullptr, r, mp, na + 1, true), rows_task(nullptr, r, nullptr, n, mp, na + 1, true),
+                     rows_task(nullptr, n, nullptr, d, m, 1, false)};
+    for (int i = 0; i < 3; ++i) {
+        p = take(4 * (size_t)t[i].segs * t[i].np * t[i].nq);
+        t[i].part = (float*)p;
+        if (w) w->task[i] = t[i];
+    }
+    return off;
 }
 
 }  // namespace moe

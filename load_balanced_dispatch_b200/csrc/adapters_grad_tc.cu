@@ -43,42 +43,46 @@ __device__ __forceinline__ void split3(float v, __nv_bfloat16 (&p)[3]) {
 
 // CTA c takes the row blocks (kRows grouped positions) c nb / grid .. (c + 1) nb / grid - 1. A group's
 // part of dB in CTA c goes to slot c + g: unique, since each next slot advances the CTA or the group.
-// Thread (te, tj) owns dB[te + 32 a][tj + 8 b].
-template <int NE, int NJ>
+// LPR lanes load a row of dh, NQ 16-byte pieces each. Thread (te, tj) owns dB[NE te + a][NJ tj + b]; du has four
+// threads a row, each a quarter of the padded rank.
+template <int NE, int NJ, int RP>
 __global__ void __launch_bounds__(asp::kThreads)
 adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hidden,
                       const __nv_bfloat16* __restrict__ bmat, const float* __restrict__ scale, int n, int r, int na,
-                      AdapterPlan plan, int nk, int planes, int64_t mp, __nv_bfloat16* __restrict__ dhp, int pc, int rp,
+                      AdapterPlan plan, int nk, int planes, int64_t mp, __nv_bfloat16* __restrict__ dhp,
                       __nv_bfloat16* __restrict__ dup, float* __restrict__ slots) {
     using namespace asp;
+    constexpr int NP = NE * 32, HS = NP + 4, US = RP + 4;  // rows 4 words apart from a multiple of 32: no bank conflicts
+    constexpr int LPR = NP == 64 ? 16 : 32, NQ = NP / (4 * LPR), JT = RP / 4, PC = RP == 32 ? 128 : 192;
+    constexpr int PASSES = kRows * LPR / kThreads;
     extern __shared__ float sm[];
-    const int hs = n | 1, us = r | 1;
-    float* sh = sm;                 // [kRows][hs] dh
-    float* su = sh + kRows * hs;    // [kRows][us] u
-    float* sb = su + kRows * us;    // [n][us] B_a
-    __shared__ int rows[kRows];
+    float* sh = sm;                 // [kRows][HS] dh
+    float* su = sh + kRows * HS;    // [kRows][US] u
+    float* sb = su + kRows * US;    // [RP][HS] B_a transposed; row j sits at (j % JT) * 4 + j / JT
     const int tid = threadIdx.x, te = tid >> 3, tj = tid & 7;
+    const int lrow = tid / LPR, lcol = tid % LPR;
     pdl_trigger();
     pdl_wait();
-    const int64_t nb = plan.goff[na + 1] / kRows, c = blockIdx.x;
-    const int64_t b0 = c * nb / gridDim.x, b1 = (c + 1) * nb / gridDim.x;
+    const int nb = plan.goff[na + 1] / kRows;
+    const int b0 = (int)((int64_t)blockIdx.x * nb / gridDim.x), b1 = (int)((int64_t)(blockIdx.x + 1) * nb / gridDim.x);
+    const bool vec = (n & 3) == 0, uvec = (r & 3) == 0;
     float acc[NE][NJ];
     int g = -1;
     auto flush = [&]() {
         if (g < 0 || g >= na) return;
-        float* out = slots + (c + g) * (int64_t)n * r;
+        float* out = slots + ((int64_t)blockIdx.x + g) * n * r;
 #pragma unroll
         for (int a = 0; a < NE; ++a)
 #pragma unroll
             for (int b = 0; b < NJ; ++b) {
-                const int e = te + 32 * a, j = tj + 8 * b;
+                const int e = NE * te + a, j = NJ * tj + b;
                 if (e < n && j < r) out[e * r + j] = acc[a][b];
             }
     };
-    for (int64_t blk = b0; blk < b1; ++blk) {
-        const int64_t p0 = blk * kRows;
-        int ng = g < 0 ? atc_group(plan.goff, na + 1, (int)p0) : g;
-        while ((int64_t)plan.goff[ng + 1] <= p0) ++ng;
+    for (int blk = b0; blk < b1; ++blk) {
+        const int p0 = blk * kRows;
+        int ng = g < 0 ? group_at(plan.goff, na + 1, p0) : g;
+        while (plan.goff[ng + 1] <= p0) ++ng;
         __syncthreads();  // the block before is done with the tiles
         if (ng != g) {
             flush();
@@ -88,54 +92,124 @@ adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hi
 #pragma unroll
                 for (int b = 0; b < NJ; ++b) acc[a][b] = 0.f;
             if (g < na)
-                for (int i = tid; i < n * r; i += kThreads)
-                    sb[i / r * us + i % r] = __bfloat162float(bmat[(int64_t)g * n * r + i]);
+                for (int i = tid; i < NP * RP; i += kThreads) {
+                    const int e = i / RP, j = i % RP;
+                    sb[((j % JT) * 4 + j / JT) * HS + e] = (e < n && j < r) ? __bfloat162float(bmat[((int64_t)g * n + e) * r + j]) : 0.f;
+                }
         }
-        if (tid < kRows) rows[tid] = plan.perm[p0 + tid];
-        __syncthreads();
-        for (int i = tid; i < kRows * n; i += kThreads) {
-            const int q = i / n, e = i - q * n;
-            sh[q * hs + e] = rows[q] >= 0 ? dh[(int64_t)rows[q] * n + e] : 0.f;
-        }
-        if (g < na)
-            for (int i = tid; i < kRows * r; i += kThreads) {
-                const int q = i / r, j = i - q * r;
-                su[q * us + j] = rows[q] >= 0 ? hidden[(int64_t)rows[q] * r + j] : 0.f;
+        // dh rows: registers -> shared memory, and their bf16 parts
+        int32_t rows[PASSES];
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) rows[i] = plan.perm[p0 + lrow + kThreads / LPR * i];
+        float4 v[PASSES][NQ];
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i)
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) {
+                const int e = 4 * (lcol + LPR * c);
+                v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (rows[i] >= 0) {
+                    const float* src = dh + (int64_t)rows[i] * n + e;
+                    if (vec) {
+                        if (e < n) v[i][c] = *reinterpret_cast<const float4*>(src);
+                    } else {
+                        if (e < n) v[i][c].x = src[0];
+                        if (e + 1 < n) v[i][c].y = src[1];
+                        if (e + 2 < n) v[i][c].z = src[2];
+                        if (e + 3 < n) v[i][c].w = src[3];
+                    }
+                }
             }
-        __syncthreads();
-        for (int i = tid; i < kRows * nk; i += kThreads) {
-            const int q = i / nk, e = i - q * nk;
-            __nv_bfloat16 p[3];
-            split3(e < n ? sh[q * hs + e] : 0.f, p);
-            for (int k = 0; k < planes; ++k) dhp[((int64_t)k * mp + p0 + q) * nk + e] = p[k];
+        if (g < na) {
+            for (int i = tid; i < kRows * (RP / 4); i += kThreads) {
+                const int q = i / (RP / 4), j = 4 * (i % (RP / 4));
+                const int32_t row = plan.perm[p0 + q];
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row >= 0 && j < r) {
+                    const float* src = hidden + (int64_t)row * r + j;
+                    if (uvec) {
+                        t = *reinterpret_cast<const float4*>(src);
+                    } else {
+                        t.x = src[0];
+                        if (j + 1 < r) t.y = src[1];
+                        if (j + 2 < r) t.z = src[2];
+                        if (j + 3 < r) t.w = src[3];
+                    }
+                }
+                *reinterpret_cast<float4*>(su + q * US + j) = t;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            const int q = lrow + kThreads / LPR * i;
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) {
+                const int e = 4 * (lcol + LPR * c);
+                *reinterpret_cast<float4*>(sh + q * HS + e) = v[i][c];
+                if (e < nk) {
+                    __nv_bfloat16 p[4][3];
+                    split3(v[i][c].x, p[0]);
+                    split3(v[i][c].y, p[1]);
+                    split3(v[i][c].z, p[2]);
+                    split3(v[i][c].w, p[3]);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        if (k < planes) {
+                            const __nv_bfloat162 lo(p[0][k], p[1][k]), hi(p[2][k], p[3][k]);
+                            *reinterpret_cast<uint2*>(dhp + ((int64_t)k * mp + p0 + q) * nk + e) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                        }
+                }
+            }
         }
         if (g >= na) continue;
-        const float s = scale[g];
-        for (int i = tid; i < kRows * rp; i += kThreads) {
-            const int q = i / rp, j = i - q * rp;
-            float t = 0.f;
-            if (j < r) {
-                for (int e = 0; e < n; ++e) t = fmaf(sh[q * hs + e], sb[e * us + j], t);
-                t *= s;
+        __syncthreads();
+        {   // du: row tid / 4, ranks (tid % 4) JT .. + JT - 1
+            const int q = tid >> 2, part = tid & 3;
+            float t[JT];
+#pragma unroll
+            for (int b = 0; b < JT; ++b) t[b] = 0.f;
+            if (part * JT < r) {
+                for (int e = 0; e < n; e += 4) {  // columns behind n are zero in both tiles
+                    const float4 h = *reinterpret_cast<const float4*>(sh + q * HS + e);
+#pragma unroll
+                    for (int b = 0; b < JT; ++b) {
+                        const float4 w = *reinterpret_cast<const float4*>(sb + (b * 4 + part) * HS + e);
+                        t[b] = fmaf(h.x, w.x, fmaf(h.y, w.y, fmaf(h.z, w.z, fmaf(h.w, w.w, t[b]))));
+                    }
+                }
             }
-            __nv_bfloat16 p[3];
-            split3(t, p);
-            __nv_bfloat16* o = dup + (p0 + q) * pc + j;
-            o[0] = p[0];
-            o[rp] = p[1];
-            o[2 * rp] = p[2];
+            const float s = scale[g];
+            __nv_bfloat16* o = dup + (int64_t)(p0 + q) * PC + part * JT;
+#pragma unroll
+            for (int b = 0; b < JT; b += 8) {
+                __nv_bfloat16 p[8][3];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) split3(s * t[b + c], p[c]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const __nv_bfloat162 two(p[2 * c][k], p[2 * c + 1][k]);
+                        u[c] = *reinterpret_cast<const uint32_t*>(&two);
+                    }
+                    *reinterpret_cast<uint4*>(o + k * RP + b) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            }
         }
         float part[NE][NJ];
 #pragma unroll
         for (int a = 0; a < NE; ++a)
 #pragma unroll
             for (int b = 0; b < NJ; ++b) part[a][b] = 0.f;
+#pragma unroll 4
         for (int q = 0; q < kRows; ++q) {
             float hv[NE], uv[NJ];
 #pragma unroll
-            for (int a = 0; a < NE; ++a) hv[a] = te + 32 * a < n ? sh[q * hs + te + 32 * a] : 0.f;
+            for (int a = 0; a < NE; a += 2) *reinterpret_cast<float2*>(hv + a) = *reinterpret_cast<const float2*>(sh + q * HS + NE * te + a);
 #pragma unroll
-            for (int b = 0; b < NJ; ++b) uv[b] = tj + 8 * b < r ? su[q * us + tj + 8 * b] : 0.f;
+            for (int b = 0; b < NJ; b += 2) *reinterpret_cast<float2*>(uv + b) = *reinterpret_cast<const float2*>(su + q * US + NJ * tj + b);
 #pragma unroll
             for (int a = 0; a < NE; ++a)
 #pragma unroll
@@ -157,20 +231,26 @@ adapters_fold_kernel(const float* __restrict__ slots, int n, int r, int d, int n
     pdl_trigger();
     pdl_wait();
     const int g = blockIdx.y;
-    const int64_t per = (int64_t)n * r;
-    const int64_t nb = plan.goff[na + 1] / kRows, b0 = plan.goff[g] / kRows, b1 = plan.goff[g + 1] / kRows;
-    const int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
+    const int per = n * r;
+    const int nb = plan.goff[na + 1] / kRows, b0 = plan.goff[g] / kRows, b1 = plan.goff[g + 1] / kRows;
+    const int i0 = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
     if (b1 == b0) {
-        for (int64_t i = i0; i < per; i += step) db[g * per + i] = 0.f;
+        for (int i = i0; i < per; i += step) db[(int64_t)g * per + i] = 0.f;
         for (int64_t i = i0; i < (int64_t)r * d; i += step) da[(int64_t)g * r * d + i] = 0.f;
         return;
     }
-    const int64_t cf = ((b0 + 1) * kGrid + nb - 1) / nb - 1, cl = (b1 * kGrid + nb - 1) / nb - 1;
-    for (int64_t i = i0; i < per; i += step) {
+    // the CTA of block b: the last c with c nb / grid <= b
+    auto cta = [&](int b) { return (int)((((int64_t)b + 1) * kGrid + nb - 1) / nb) - 1; };
+    for (int i = i0; i < per; i += step) {
         float t = 0.f;
-        for (int64_t c = cf; c <= cl; ++c)
-            if ((c + 1) * nb / kGrid > c * nb / kGrid) t += slots[(c + g) * per + i];  // with few blocks some CTAs have none
-        db[g * per + i] = scale[g] * t;
+        if (nb >= kGrid) {  // every CTA has blocks: those of the group follow one another
+            const int cf = cta(b0), cl = cta(b1 - 1);
+#pragma unroll 4
+            for (int c = cf; c <= cl; ++c) t += slots[((int64_t)c + g) * per + i];
+        } else {            // a CTA has one block at most
+            for (int b = b0; b < b1; ++b) t += slots[((int64_t)cta(b) + g) * per + i];
+        }
+        db[(int64_t)g * per + i] = scale[g] * t;
     }
 }
 
@@ -246,7 +326,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
     // row tile -> group, first grouped position, rows (0: nothing to do)
     auto rows_of = [&](int64_t tile, int& g, int& p0) -> int {
         const int t = (int)(tile / SUB);
-        g = atc_group(plan.tstart, groups, t);
+        g = group_at(plan.tstart, groups, t);
         p0 = plan.goff[g] + 256 * (t - plan.tstart[g]) + 128 * (int)(tile % SUB);
         const int cnt = plan.goff[g] + plan.gcnt[g] - p0;
         return cnt < 0 ? 0 : min(cnt, 128 * MH);
@@ -506,7 +586,7 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
         if (one) {
             u.nkb = plan.goff[na + 1] / BK;
         } else {
-            u.g = atc_group(plan.goff, na, (int)(pos / U) * BK);  // the last group that starts there: not empty
+            u.g = group_at(plan.goff, na, (int)(pos / U) * BK);  // the last group that starts there: not empty
             u.blk0 = plan.goff[u.g] / BK;
             u.nkb = plan.goff[u.g + 1] / BK - u.blk0;
         }
@@ -729,18 +809,12 @@ static size_t agt_layout(int64_t m, int d, int n, int r, int na, AgtWs* w, char*
     return off;
 }
 
-// set on every call: the attribute belongs to the current device
-template <typename K>
-static cudaError_t need_smem(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <int MH, int ND, int NC, int RP>
 static cudaError_t launch_adx(const CUtensorMap& mdh, const CUtensorMap& mdu, const CUtensorMap& mw,
                               const CUtensorMap& ma, int d, int n, int r, int na, const AdapterPlan& plan,
                               __nv_bfloat16* dx, cudaStream_t stream) {
     constexpr size_t smem = AdxTile<MH, ND, NC, RP>::SMEM;
-    const cudaError_t e = need_smem(adapters_dx_tc_kernel<MH, ND, NC, RP>, smem);
+    const cudaError_t e = need_smem<adapters_dx_tc_kernel<MH, ND, NC, RP>>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(adapters_dx_tc_kernel<MH, ND, NC, RP>, dim3(kNumSMs), dim3(adx::kThreads), smem, stream, mdh, mdu,
                       mw, ma, d, n, r, na, plan, dx);
@@ -751,20 +825,20 @@ static cudaError_t launch_rct(const CUtensorMap& mx, const CUtensorMap& mg, cons
                               int na, int one, const AdapterPlan& plan, float* part, int32_t* tickets, float* out,
                               int64_t gs, int64_t cs, int64_t ds, cudaStream_t stream) {
     constexpr size_t smem = RctTile<C>::SMEM;
-    const cudaError_t e = need_smem(rows_contract_tc_kernel<C>, smem);
+    const cudaError_t e = need_smem<rows_contract_tc_kernel<C>>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(rows_contract_tc_kernel<C>, dim3(kNumSMs), dim3(rct::kThreads), smem, stream, mx, mg, mp, d, ncols,
                       na, one, plan, part, tickets, out, gs, cs, ds);
 }
 
-template <int NE, int NJ>
+template <int NE, int NJ, int RP>
 static cudaError_t launch_split(const float* dh, const float* hidden, const __nv_bfloat16* b, const float* scale, int n,
                                 int r, int na, const AgtShape& s, const AgtWs& w, int planes, cudaStream_t stream) {
-    const size_t smem = sizeof(float) * ((size_t)asp::kRows * ((n | 1) + (r | 1)) + (size_t)n * (r | 1));
-    const cudaError_t e = need_smem(adapters_split_kernel<NE, NJ>, smem);
+    constexpr size_t smem = sizeof(float) * ((size_t)(asp::kRows + RP) * (NE * 32 + 4) + (size_t)asp::kRows * (RP + 4));
+    const cudaError_t e = need_smem<adapters_split_kernel<NE, NJ, RP>>(smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(adapters_split_kernel<NE, NJ>, dim3(asp::kGrid), dim3(asp::kThreads), smem, stream, dh, hidden, b,
-                      scale, n, r, na, w.plan, s.nk, planes, s.mp, w.dhp, s.pc, s.rp, w.dup, w.slots);
+    return launch_pdl(adapters_split_kernel<NE, NJ, RP>, dim3(asp::kGrid), dim3(asp::kThreads), smem, stream, dh, hidden,
+                      b, scale, n, r, na, w.plan, s.nk, planes, s.mp, w.dhp, w.dup, w.slots);
 }
 
 static cudaError_t launch_adapters_grad_tc(const float* dh, const __nv_bfloat16* x, const float* w_r,
@@ -775,12 +849,13 @@ static cudaError_t launch_adapters_grad_tc(const float* dh, const __nv_bfloat16*
     const AgtShape s = agt_shape(m, d, n, r, na);
     AgtWs w;
     agt_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
-    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, w.tickets, s.tickets_a + s.tickets_w, w_r, d, n, s.nk, 2,
-                                        dx ? w.wparts : nullptr, stream);
+    PrepExtra extra = {};
+    extra.w_r = w_r; extra.d = d; extra.n = n; extra.nk = s.nk; extra.parts = 2; extra.wparts = dx ? w.wparts : nullptr;
+    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, w.tickets, s.tickets_a + s.tickets_w, extra, stream);
     if (e != cudaSuccess) return e;
     const int planes = dw_r ? 3 : 2;
-#define MOE_SPLIT(NE, NJ) e = launch_split<NE, NJ>(dh, hidden, b, scale, n, r, na, s, w, planes, stream)
-#define MOE_SPLIT_R(NE) do { if (r <= 16) MOE_SPLIT(NE, 2); else if (r <= 32) MOE_SPLIT(NE, 4); else MOE_SPLIT(NE, 8); } while (0)
+#define MOE_SPLIT(NE, NJ, RP) e = launch_split<NE, NJ, RP>(dh, hidden, b, scale, n, r, na, s, w, planes, stream)
+#define MOE_SPLIT_R(NE) do { if (r <= 16) MOE_SPLIT(NE, 2, 32); else if (r <= 32) MOE_SPLIT(NE, 4, 32); else MOE_SPLIT(NE, 8, 64); } while (0)
     if (n <= 64) MOE_SPLIT_R(2);
     else if (n <= 128) MOE_SPLIT_R(4);
     else MOE_SPLIT_R(8);

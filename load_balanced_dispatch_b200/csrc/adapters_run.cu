@@ -50,23 +50,29 @@ static cudaError_t launch_adapters_grad_f32(const float* dh, const float* x, con
                                             float* da, float* db, float* dw_r, void* workspace, cudaStream_t stream) {
     AdapterWs w;
     adapter_ws_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
-    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, nullptr, 0, nullptr, 0, 0, 0, 0, nullptr, stream);
-    if (e != cudaSuccess) return e;
-    const int rows = adp::kThreads / 32;
-    e = launch_pdl(adapters_du_kernel, dim3((unsigned)((m + rows - 1) / rows)), dim3(adp::kThreads), 0, stream, dh, b,
-                   idx, scale, m, n, r, na, w.du);
+    PrepExtra extra = {};
+    extra.dh = dh; extra.b = b; extra.scale = scale; extra.n = n; extra.r = r; extra.du = w.du;
+    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, nullptr, 0, extra, stream);
     if (e != cudaSuccess) return e;
     if (dx) {
         e = launch_pdl(adapters_dx_kernel, dim3((unsigned)((m + 15) / 16), (unsigned)((d + 127) / 128)),
                        dim3(adp::kThreads), 0, stream, dh, w_r, a, idx, w.du, m, d, n, r, na, dx);
         if (e != cudaSuccess) return e;
     }
-    e = launch_rows_contract(x, d, w.du, r, m, na, w.plan, nullptr, w.part, da, stream);
+    RowsTasks tasks = {};
+    tasks.count = dw_r ? 3 : 2;
+    const float *X[3] = {x, hidden, dh}, *Y[3] = {w.du, dh, x}, *S[3] = {nullptr, scale, nullptr};
+    float* out[3] = {da, db, dw_r};
+    int64_t blocks = 0, fold = 0;
+    for (int i = 0; i < tasks.count; ++i) {
+        RowsTask& t = tasks.t[i] = w.task[i];
+        t.X = X[i]; t.Y = Y[i]; t.scale = S[i]; t.out = out[i];
+        blocks += (int64_t)t.ptiles * t.qtiles * t.segs;
+        fold += ((int64_t)t.np * t.nq + adp::kThreads - 1) / adp::kThreads;
+    }
+    e = launch_pdl(rows_outer_kernel, dim3((unsigned)blocks), dim3(adp::kThreads), 0, stream, tasks, m, na + 1, w.plan);
     if (e != cudaSuccess) return e;
-    e = launch_rows_contract(hidden, r, dh, n, m, na, w.plan, scale, w.part, db, stream);
-    if (e != cudaSuccess || !dw_r) return e;
-    AdapterPlan none = {};
-    return launch_rows_contract(dh, n, x, d, m, na, none, nullptr, w.part, dw_r, stream);
+    return launch_pdl(rows_fold_kernel, dim3((unsigned)fold, (unsigned)na), dim3(adp::kThreads), 0, stream, tasks, w.plan);
 }
 
 cudaError_t launch_router_adapters_grad(const float* dh, const void* x, moe_dtype dt, const float* w_r, const void* a,

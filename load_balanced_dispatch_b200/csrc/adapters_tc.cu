@@ -60,16 +60,6 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
-// Largest g in [0, groups) with start[g] <= t.
-__device__ __forceinline__ int atc_group(const int32_t* __restrict__ start, int groups, int t) {
-    int lo = 0, hi = groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= t) lo = mid; else hi = mid;
-    }
-    return lo;
-}
-
 template <int NP, int RP>
 __global__ void __launch_bounds__(atc::kThreads, 1)
 router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
@@ -119,7 +109,7 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
     auto rows_of = [&](int64_t unit, int& ct, int& g, int& p0) -> int {
         const int tile = (int)(unit / nct);
         ct = (int)(unit % nct);
-        g = atc_group(plan.tstart, groups, tile);
+        g = group_at(plan.tstart, groups, tile);
         p0 = plan.goff[g] + BM * (tile - plan.tstart[g]);
         const int cnt = plan.goff[g] + plan.gcnt[g] - p0;
         return cnt < BM ? cnt : BM;
@@ -424,9 +414,7 @@ static cudaError_t launch_atc(const CUtensorMap& mx, const CUtensorMap& mg, cons
                               const CUtensorMap& ma, const __nv_bfloat16* b, const float* scale, int d, int n, int r,
                               int na, int nct, const AtcWs& w, float* logits, float* hidden, cudaStream_t stream) {
     constexpr size_t smem = AtcTile<NP, RP>::SMEM;
-    // set on every call: the attribute belongs to the current device
-    const cudaError_t e = cudaFuncSetAttribute(router_adapters_tc_kernel<NP, RP>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = need_smem<router_adapters_tc_kernel<NP, RP>>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(router_adapters_tc_kernel<NP, RP>, dim3(kNumSMs), dim3(atc::kThreads), smem, stream, mx, mg, mw,
                       ma, b, scale, d, n, r, na, nct, w.plan, w.part, w.tickets, logits, hidden);
@@ -440,8 +428,9 @@ static cudaError_t launch_router_adapters_tc(const __nv_bfloat16* x, const float
     atc_tile(n, r, np, rp, nct);
     AtcWs w;
     atc_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
-    cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, w.tickets, atc_tiles(m, na) * nct, w_r, d, n, 0, 3, w.wsplit,
-                                       stream);
+    PrepExtra extra = {};
+    extra.w_r = w_r; extra.d = d; extra.n = n; extra.parts = 3; extra.wparts = w.wsplit;
+    const cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, w.tickets, atc_tiles(m, na) * nct, extra, stream);
     if (e != cudaSuccess) return e;
     CUtensorMap mx, mg, mw, ma;
     if (!map_2d(&mx, x, (uint64_t)m, (uint64_t)d, 32) || !map_2d(&mg, x, (uint64_t)m, (uint64_t)d, 1) ||

@@ -104,10 +104,10 @@ __device__ __forceinline__ float lanes_max(float v) {
     return v;
 }
 
-// e_j = exp(h_j - top) / sum and the log-sum-exp of a row held by L lanes. A row whose logits are
-// all -inf has no scores: e = 0 and lse = 0. NaN and +inf give NaN.
+// h_j <- exp(h_j - top) / sum, and the log-sum-exp of a row held by L lanes. A row whose logits are
+// all -inf has no scores: 0 throughout and lse = 0. NaN and +inf give NaN.
 template <int L, int V>
-__device__ __forceinline__ void row_softmax(const float (&h)[4 * V], float (&e)[4 * V], float& lse) {
+__device__ __forceinline__ float row_softmax(float (&h)[4 * V]) {
     float top = h[0];
 #pragma unroll
     for (int q = 1; q < 4 * V; ++q) top = fmaxf(top, h[q]);
@@ -115,18 +115,17 @@ __device__ __forceinline__ void row_softmax(const float (&h)[4 * V], float (&e)[
     float s = 0.f;
     if (top == -INFINITY) {  // fmaxf passes over NaN: keep it in the sum
 #pragma unroll
-        for (int q = 0; q < 4 * V; ++q) { e[q] = h[q] == -INFINITY ? 0.f : h[q]; s += e[q]; }
-        s = lanes_sum<L>(s);
-        lse = s;
-        return;
-    }
+        for (int q = 0; q < 4 * V; ++q) { h[q] = h[q] == -INFINITY ? 0.f : h[q]; s += h[q]; }
+    } else {
 #pragma unroll
-    for (int q = 0; q < 4 * V; ++q) { e[q] = expf(h[q] - top); s += e[q]; }
+        for (int q = 0; q < 4 * V; ++q) { h[q] = expf(h[q] - top); s += h[q]; }
+    }
     s = lanes_sum<L>(s);
+    if (top == -INFINITY) return s;
     const float inv = 1.f / s;
 #pragma unroll
-    for (int q = 0; q < 4 * V; ++q) e[q] *= inv;
-    lse = top + logf(s);
+    for (int q = 0; q < 4 * V; ++q) h[q] *= inv;
+    return top + logf(s);
 }
 
 __device__ __forceinline__ float logistic(float h) { return 1.f / (1.f + expf(-h)); }
@@ -139,18 +138,20 @@ router_loss_chunk_kernel(const float* __restrict__ logits, const int32_t* __rest
     using namespace rloss;
     constexpr int RW = 32 / L;                      // rows a warp holds
     constexpr int GROUPS = (kThreads / 32) * RW;    // rows the CTA holds at a time
-    extern __shared__ double fold[];                // [GROUPS][4 V L + 1] a row group's sums
-    __shared__ int cnt[kMaxExperts];
+    constexpr int U = GROUPS >= 64 ? 1 : 4;         // rows in flight per lane group
+    constexpr int FS = 4 * V * L + 1;
+    extern __shared__ double fold[];                // [GROUPS][FS] a row group's sums
+    __shared__ double tot_p[kMaxExperts];
+    __shared__ int cnt[kMaxExperts], tot_c[kMaxExperts];
     __shared__ double zpart[GROUPS];
     __shared__ int ntok;
     const int tid = threadIdx.x, lane = tid & 31, sub = lane % L, grp = (tid >> 5) * RW + lane / L;
-    constexpr int FS = 4 * V * L + 1;
     const bool vec = (n & 3) == 0;
     pdl_trigger();
     pdl_wait();
     const int64_t c = blockIdx.x, r0 = c * kRows, r1 = min(r0 + (int64_t)kRows, m);
     if (c == 0 && tid == 0) *w.ticket = 0;
-    for (int e = tid; e < n; e += kThreads) { w.tsum[c * n + e] = 0.0; w.tcnt[c * n + e] = 0; }
+    if (tid < n) { tot_p[tid] = 0.0; tot_c[tid] = 0; }
     double z = 0.0;
     int total = 0;
     for (int64_t at = r0; at < r1;) {
@@ -158,35 +159,64 @@ router_loss_chunk_kernel(const float* __restrict__ logits, const int32_t* __rest
         if (s >= nseq) break;                                        // behind the last sequence
         const int64_t next = min((int64_t)off[s + 1], r1);           // > at: off[s + 1] is the first offset above it
         if (s < 0) { at = next; continue; }                          // before the first
-        for (int e = tid; e < n; e += kThreads) cnt[e] = 0;
+        if (tid < n) cnt[tid] = 0;
         if (tid == 0) ntok = 0;
         __syncthreads();
         double acc[4 * V];
 #pragma unroll
         for (int q = 0; q < 4 * V; ++q) acc[q] = 0.0;
         // every lane of a warp runs the same number of rounds: the row's lanes reduce together
-        for (int64_t base = at; base < next; base += GROUPS) {
-            const int64_t r = base + grp;
-            const bool live = r < next && (!mask || mask[r]);
-            float h[4 * V], p[4 * V];
+        for (int64_t base = at; base < next; base += GROUPS * U) {
+            bool live[U];
+            int pick[U];
+            float h[U][4 * V];
 #pragma unroll
-            for (int q = 0; q < 4 * V; ++q) h[q] = -INFINITY;
-            if (live) load_row<L, V>(logits + r * n, n, vec, sub, h);
-            float lse = 0.f;
-            if (fn == MOE_SOFTMAX || want_z) row_softmax<L, V>(h, p, lse);
-            if (fn == MOE_SIGMOID) {
-#pragma unroll
-                for (int q = 0; q < 4 * V; ++q) p[q] = logistic(h[q]);
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = base + grp + GROUPS * u;
+                live[u] = r < next && (!mask || mask[r]);
             }
-            if (live) {
 #pragma unroll
-                for (int q = 0; q < 4 * V; ++q) acc[q] += (double)p[q];
-                if (sub == 0) { z += (double)lse * (double)lse; atomicAdd(&ntok, 1); }
-                for (int t = sub; t < k; t += L) {
-                    const int e = idx[r * k + t];
-                    if (e < 0 || e >= n) record_error(kErrExpertIndex);
-                    else atomicAdd(&cnt[e], 1);
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = base + grp + GROUPS * u;
+#pragma unroll
+                for (int q = 0; q < 4 * V; ++q) h[u][q] = -INFINITY;
+                if (live[u]) load_row<L, V>(logits + r * n, n, vec, sub, h[u]);
+                pick[u] = live[u] && sub < k ? idx[r * k + sub] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (fn == MOE_SIGMOID) {
+                    float e[4 * V];
+#pragma unroll
+                    for (int q = 0; q < 4 * V; ++q) e[q] = h[u][q];
+                    if (want_z) {
+                        const float lse = row_softmax<L, V>(e);
+                        if (sub == 0) z += (double)lse * (double)lse;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4 * V; ++q) h[u][q] = live[u] ? logistic(h[u][q]) : 0.f;
+                } else {
+                    const float lse = row_softmax<L, V>(h[u]);
+                    if (sub == 0) z += (double)lse * (double)lse;
                 }
+                if (live[u]) {
+                    const int64_t r = base + grp + GROUPS * u;
+                    if (sub == 0) atomicAdd(&ntok, 1);
+                    int e = pick[u];
+                    for (int t = sub; t < k;) {
+                        if (e < 0 || e >= n) record_error(kErrExpertIndex);
+                        else atomicAdd(&cnt[e], 1);
+                        t += L;
+                        if (t < k) e = idx[r * k + t];
+                    }
+                }
+            }
+            // U scores are added in fp32, the sums over the rounds in fp64
+#pragma unroll
+            for (int q = 0; q < 4 * V; ++q) {
+                float t = h[0][q];
+                if constexpr (U == 4) t = (h[0][q] + h[1][q]) + (h[2][q] + h[3][q]);
+                acc[q] += (double)t;
             }
         }
         // column 4 (sub + L v) + q of row group g sits at fold[g][4 (sub + L v) + q]
@@ -196,19 +226,21 @@ router_loss_chunk_kernel(const float* __restrict__ logits, const int32_t* __rest
             for (int q = 0; q < 4; ++q) fold[grp * FS + 4 * (sub + L * v) + q] = acc[4 * v + q];
         __syncthreads();
         const int64_t slot = c + s;
-        for (int e = tid; e < n; e += kThreads) {
+        if (tid < n) {
             double t = 0.0;
-            for (int g = 0; g < GROUPS; ++g) t += fold[g * FS + e];
-            w.psum[slot * n + e] = t;
-            w.pcnt[slot * n + e] = cnt[e];
-            w.tsum[c * n + e] += t;
-            w.tcnt[c * n + e] += cnt[e];
+#pragma unroll 8
+            for (int g = 0; g < GROUPS; ++g) t += fold[g * FS + tid];
+            w.psum[slot * n + tid] = t;
+            w.pcnt[slot * n + tid] = cnt[tid];
+            tot_p[tid] += t;
+            tot_c[tid] += cnt[tid];
         }
         if (tid == 0) { w.ptok[slot] = ntok; total += ntok; }
         __syncthreads();
         at = next;
     }
     if (sub == 0) zpart[grp] = z;
+    if (tid < n) { w.tsum[c * n + tid] = tot_p[tid]; w.tcnt[c * n + tid] = tot_c[tid]; }
     __syncthreads();
     if (tid == 0) {
         double t = 0.0;
@@ -320,7 +352,8 @@ router_loss_fold_kernel(int64_t m, int n, int k, const int32_t* __restrict__ off
 
 // dL/dp_j of a token of sequence s, f held fixed: g_j = up (alpha n f^G_j / T + alpha_seq n f^s_j / (S' T_s)).
 // For softmax, p_j (g_j - sum_i p_i g_i) does not change when a constant is taken from every g, so
-// f - 1/n stands for f: near balance the difference keeps its digits.
+// f - 1/n = (count n - k T) / (k T n) stands for f (an exact whole number over a constant): near balance the
+// difference keeps its digits. A lane group takes consecutive rows, two in flight.
 template <int L, int V>
 __global__ void __launch_bounds__(rloss::kThreads)
 router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx, int64_t m, int n, int k,
@@ -329,157 +362,199 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
                         const int32_t* __restrict__ tokens, const float* __restrict__ dloss,
                         const float* __restrict__ dgate, int renorm, float* __restrict__ dlogits) {
     using namespace rloss;
-    constexpr int RW = 32 / L, GROUPS = (kThreads / 32) * RW;
-    extern __shared__ float scat[];  // [GROUPS][4 V L]: what the gates add to each column of the row
+    constexpr int RW = 32 / L, GROUPS = (kThreads / 32) * RW, U = 2;
+    constexpr int CW = 4 * V * L;
+    extern __shared__ float scat[];  // [GROUPS][CW]: a row's logits for its picks, then what the gates add to each column
     __shared__ int s_full;
     const int tid = threadIdx.x, lane = tid & 31, sub = lane % L, grp = (tid >> 5) * RW + lane / L;
-    constexpr int CW = 4 * V * L;
     const bool vec = (n & 3) == 0;
     pdl_trigger();
     pdl_wait();
-    if (tid == 0) s_full = 0;
-    __syncthreads();
     if (alpha_seq != 0.0) {
+        if (tid == 0) s_full = 0;
+        __syncthreads();
         int full = 0;
         for (int q = tid; q < nseq; q += kThreads) full += tokens[q] > 0;
         if (full) atomicAdd(&s_full, full);
+        __syncthreads();
     }
     float* mine = scat + grp * CW;
     if (dgate)
         for (int j = sub; j < CW; j += L) mine[j] = 0.f;
-    __syncthreads();
+    __syncwarp();
     const double up = dloss ? (double)*dloss : 1.0;
-    const double T = (double)max(tokens[nseq], 1);
-    const double shift = fn == MOE_SOFTMAX ? 1.0 / (double)n : 0.0;
+    const int T = max(tokens[nseq], 1);
+    const bool soft = fn == MOE_SOFTMAX;
     const float cz = (float)(2.0 * z_coef * up / T);
-    const bool chosen = fn == MOE_SOFTMAX && renorm && k > 1;  // gate = softmax over the picks
-    // g's constants: the whole batch's part of each owned column
-    float gG[4 * V], gs[4 * V];
+    const bool chosen = soft && renorm && k > 1;  // gate = softmax over the picks
+    const double full = alpha_seq != 0.0 ? (double)max(s_full, 1) : 1.0;
+    // a table row's part of g for the owned columns: coef / T * (count n - k T) / (k T), or coef / T * count n / (k T)
+    auto table = [&](const int32_t* row, int64_t t, double coef, float (&g)[4 * V]) {
+        const float scale = (float)(coef / ((double)t * (double)t * (double)k));
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int j = 4 * (sub + L * v) + q;
-            gG[4 * v + q] = 0.f;
-            gs[4 * v + q] = 0.f;
-            if (j < n)
-                gG[4 * v + q] = (float)(up * alpha * n / T * ((double)counts[(int64_t)nseq * n + j] / (k * T) - shift));
-        }
-    const int64_t per = (m + gridDim.x - 1) / gridDim.x;  // rows of this CTA, consecutive
-    const int64_t r0 = blockIdx.x * per, r1 = min(r0 + per, m);
+            for (int q = 0; q < 4; ++q) {
+                const int j = 4 * (sub + L * v) + q;
+                g[4 * v + q] = j < n ? scale * (float)((int64_t)row[j] * n - (soft ? (int64_t)k * t : 0)) : 0.f;
+            }
+    };
+    float gG[4 * V], gt[4 * V];  // the whole batch's part; with the row's sequence
+    table(counts + (int64_t)nseq * n, T, up * alpha, gG);
+#pragma unroll
+    for (int q = 0; q < 4 * V; ++q) gt[q] = gG[q];
+    const int64_t groups = (int64_t)gridDim.x * GROUPS, per = (m + groups - 1) / groups;
+    const int64_t r0 = ((int64_t)blockIdx.x * GROUPS + grp) * per, r1 = min(r0 + per, m);
     int seq = -2;
     int64_t seq_end = -1;  // the rows below it that follow the current one belong to `seq`
-    for (int64_t base = r0; base < r1; base += GROUPS) {
-        const int64_t r = base + grp;
-        const bool in = r < r1;
-        if (in && r >= seq_end) {
-            seq = seq_of_row(off, nseq, r);
-            seq_end = seq >= nseq ? m : (int64_t)off[seq + 1];
-            if (alpha_seq != 0.0 && seq >= 0 && seq < nseq) {
-                const double Ts = (double)max(tokens[seq], 1);
-                const double cs = up * alpha_seq * n / ((double)max(s_full, 1) * Ts);
+    // every lane of a warp runs the same number of rounds: the row's lanes reduce together
+    for (int64_t i = 0; i < per; i += U) {
+        float h[U][4 * V], dg[U];
+        int pick[U];
+        bool live[U];
+        bool ok[U];
 #pragma unroll
-                for (int v = 0; v < V; ++v)
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + i + u;
+            ok[u] = i + u < per && r < r1 && (!mask || mask[r]);
+        }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int j = 4 * (sub + L * v) + q;
-                        if (j < n) gs[4 * v + q] = (float)(cs * ((double)counts[(int64_t)seq * n + j] / (k * Ts) - shift));
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + i + u;
+#pragma unroll
+            for (int q = 0; q < 4 * V; ++q) h[u][q] = -INFINITY;
+            if (ok[u]) load_row<L, V>(logits + r * n, n, vec, sub, h[u]);
+            const bool has = ok[u] && dgate && sub < k;
+            pick[u] = has ? idx[r * k + sub] : -1;
+            dg[u] = has ? dgate[r * k + sub] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + i + u;
+            const bool in = i + u < per && r < r1;
+            if (in && r >= seq_end) {
+                seq = seq_of_row(off, nseq, r);
+                seq_end = seq >= nseq ? m : (int64_t)off[seq + 1];
+                if (alpha_seq != 0.0 && seq >= 0 && seq < nseq) {
+                    table(counts + (int64_t)seq * n, max(tokens[seq], 1), up * alpha_seq / full, gt);
+#pragma unroll
+                    for (int q = 0; q < 4 * V; ++q) gt[q] += gG[q];
+                }
+            }
+            live[u] = ok[u] && seq >= 0 && seq < nseq;
+            float add[4 * V];
+#pragma unroll
+            for (int q = 0; q < 4 * V; ++q) add[q] = 0.f;
+            if (dgate) {
+                if (chosen) {
+                    // q_r = softmax over the picks' logits; dL/dh = q_r (dg_r - sum q dg)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        *reinterpret_cast<float4*>(mine + 4 * (sub + L * v)) =
+                            make_float4(h[u][4 * v], h[u][4 * v + 1], h[u][4 * v + 2], h[u][4 * v + 3]);
+                    __syncwarp();
+                    const int e0 = live[u] && pick[u] >= 0 && pick[u] < n ? pick[u] : -1;
+                    const float x0 = e0 >= 0 ? mine[e0] : -INFINITY;
+                    float top = x0;
+                    for (int t = sub + L; t < k; t += L) {
+                        const int e = live[u] ? idx[r * k + t] : -1;
+                        if (e >= 0 && e < n) top = fmaxf(top, mine[e]);
                     }
-            }
-        }
-        const bool live = in && seq >= 0 && seq < nseq && (!mask || mask[r]);
-        float h[4 * V], p[4 * V], soft[4 * V], out[4 * V];
-#pragma unroll
-        for (int q = 0; q < 4 * V; ++q) h[q] = -INFINITY;
-        if (live) load_row<L, V>(logits + r * n, n, vec, sub, h);
-        float lse = 0.f;
-        if (fn == MOE_SOFTMAX || cz != 0.f) row_softmax<L, V>(h, soft, lse);
-        float g[4 * V];
-#pragma unroll
-        for (int q = 0; q < 4 * V; ++q) g[q] = gG[q] + gs[q];
-        if (dgate) {
-            if (chosen) {
-                // q_r = softmax over the picks' logits; dL/dh = q_r (dg_r - sum q dg)
-                float top = -INFINITY, sum = 0.f, dot = 0.f;
-                for (int t = sub; t < k; t += L) {
-                    const int e = live ? idx[r * k + t] : -1;
-                    if (e >= 0 && e < n) top = fmaxf(top, logits[r * n + e]);
-                }
-                top = lanes_max<L>(top);
-                for (int t = sub; t < k; t += L) {
-                    const int e = live ? idx[r * k + t] : -1;
-                    if (e >= 0 && e < n && top != -INFINITY) {
-                        const float x = expf(logits[r * n + e] - top);
-                        sum += x;
-                        dot = fmaf(x, dgate[r * k + t], dot);
+                    top = lanes_max<L>(top);
+                    if (top == -INFINITY) top = 0.f;  // no pick has a score: every weight is 0
+                    const float w0 = expf(x0 - top);
+                    float sum = w0, dot = w0 * dg[u];
+                    for (int t = sub + L; t < k; t += L) {
+                        const int e = live[u] ? idx[r * k + t] : -1;
+                        if (e >= 0 && e < n) {
+                            const float x = expf(mine[e] - top);
+                            sum += x;
+                            dot = fmaf(x, dgate[r * k + t], dot);
+                        }
                     }
-                }
-                sum = lanes_sum<L>(sum);
-                dot = lanes_sum<L>(dot) / sum;
-                for (int t = sub; t < k; t += L) {
-                    const int e = live ? idx[r * k + t] : -1;
-                    if (e >= 0 && e < n && top != -INFINITY)
-                        atomicAdd(&mine[e], expf(logits[r * n + e] - top) / sum * (dgate[r * k + t] - dot));
-                }
-            } else {
-                for (int t = sub; t < k; t += L) {
-                    const int e = live ? idx[r * k + t] : -1;
-                    if (e >= 0 && e < n) atomicAdd(&mine[e], dgate[r * k + t]);
-                }
-            }
-            __syncwarp();
-            // read the row's columns and clear them for the next row
+                    sum = lanes_sum<L>(sum);
+                    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+                    dot = lanes_sum<L>(dot) * inv;
+                    // further picks (k > L): their terms wait in registers of the second pass over the row's logits
+                    float keep[4 * V];
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+                    for (int q = 0; q < 4 * V; ++q) keep[q] = 0.f;
+                    if (k > L) {
+                        // column j's term, from the picks that name it: each lane looks at every pick
+                        for (int t = 0; t < k; ++t) {
+                            const int e = live[u] ? idx[r * k + t] : -1;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int j = 4 * (sub + L * v) + q;
-                    out[4 * v + q] = mine[j];
-                    mine[j] = 0.f;
-                }
-            __syncwarp();
-        } else {
+                            for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int q = 0; q < 4 * V; ++q) out[q] = 0.f;
-        }
-        if (!chosen) {
+                                for (int q = 0; q < 4; ++q)
+                                    if (e == 4 * (sub + L * v) + q && e < n)
+                                        keep[4 * v + q] += expf(h[u][4 * v + q] - top) * inv * (dgate[r * k + t] - dot);
+                        }
+                    }
+                    __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 4 * V; ++q) { g[q] += out[q]; out[q] = 0.f; }
-        }
-        if (fn == MOE_SOFTMAX) {
-            float c = 0.f;
-#pragma unroll
-            for (int q = 0; q < 4 * V; ++q) c = fmaf(soft[q], g[q], c);
-            c = lanes_sum<L>(c);
-#pragma unroll
-            for (int q = 0; q < 4 * V; ++q) out[q] = fmaf(soft[q], g[q] - c, out[q]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4 * V; ++q) {
-                p[q] = logistic(h[q]);
-                out[q] = g[q] * p[q] * logistic(-h[q]);  // 1 - rho from its own exponential: exact for large h
-            }
-        }
-        if (cz != 0.f) {
-#pragma unroll
-            for (int q = 0; q < 4 * V; ++q) out[q] = fmaf(cz * lse, soft[q], out[q]);
-        }
-        if (in) {
-            float* row = dlogits + r * n;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int j = 4 * (sub + L * v);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (!live) out[4 * v + q] = 0.f;
-                if (vec) {
-                    if (j < n)
-                        *reinterpret_cast<float4*>(row + j) =
-                            make_float4(out[4 * v], out[4 * v + 1], out[4 * v + 2], out[4 * v + 3]);
+                    for (int v = 0; v < V; ++v)
+                        *reinterpret_cast<float4*>(mine + 4 * (sub + L * v)) = make_float4(keep[4 * v], keep[4 * v + 1], keep[4 * v + 2], keep[4 * v + 3]);
+                    __syncwarp();
+                    if (k <= L && e0 >= 0) atomicAdd(&mine[e0], w0 * inv * (dg[u] - dot));
                 } else {
+                    if (live[u] && pick[u] >= 0 && pick[u] < n) atomicAdd(&mine[pick[u]], dg[u]);
+                    for (int t = sub + L; t < k; t += L) {
+                        const int e = live[u] ? idx[r * k + t] : -1;
+                        if (e >= 0 && e < n) atomicAdd(&mine[e], dgate[r * k + t]);
+                    }
+                }
+                __syncwarp();
+                // read the row's columns and clear them for the next row
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float4* at = reinterpret_cast<float4*>(mine + 4 * (sub + L * v));
+                    const float4 t = *at;
+                    *at = make_float4(0.f, 0.f, 0.f, 0.f);
+                    add[4 * v] = t.x; add[4 * v + 1] = t.y; add[4 * v + 2] = t.z; add[4 * v + 3] = t.w;
+                }
+                __syncwarp();
+            }
+            float out[4 * V];
+            if (soft) {
+                const float lse = row_softmax<L, V>(h[u]);  // h is the score now
+                float c = 0.f;
+                float g[4 * V];
+#pragma unroll
+                for (int q = 0; q < 4 * V; ++q) {
+                    g[q] = gt[q] + (chosen ? 0.f : add[q]);
+                    c = fmaf(h[u][q], g[q], c);
+                }
+                c = lanes_sum<L>(c);
+#pragma unroll
+                for (int q = 0; q < 4 * V; ++q) out[q] = fmaf(h[u][q], g[q] - c + cz * lse, chosen ? add[q] : 0.f);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4 * V; ++q)  // 1 - rho from its own exponential: exact for large h
+                    out[q] = (gt[q] + add[q]) * logistic(h[u][q]) * logistic(-h[u][q]);
+                if (cz != 0.f) {
+                    const float lse = row_softmax<L, V>(h[u]);
+#pragma unroll
+                    for (int q = 0; q < 4 * V; ++q) out[q] = fmaf(cz * lse, h[u][q], out[q]);
+                }
+            }
+            if (in) {
+                float* row = dlogits + r * n;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int j = 4 * (sub + L * v);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        if (j + q < n) row[j + q] = out[4 * v + q];
+                        if (!live[u]) out[4 * v + q] = 0.f;
+                    if (vec) {
+                        if (j < n)
+                            *reinterpret_cast<float4*>(row + j) =
+                                make_float4(out[4 * v], out[4 * v + 1], out[4 * v + 2], out[4 * v + 3]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (j + q < n) row[j + q] = out[4 * v + q];
+                    }
                 }
             }
         }
@@ -533,7 +608,7 @@ cudaError_t launch_router_loss_grad(const float* logits, const int32_t* idx, int
     do {                                                                                                             \
         constexpr int G = (rloss::kThreads / 32) * (32 / L);                                                         \
         int64_t blocks = (m + G - 1) / G;                                                                            \
-        if (blocks > (int64_t)kNumSMs * 4) blocks = (int64_t)kNumSMs * 4;                                            \
+        if (blocks > (int64_t)kNumSMs * 6) blocks = (int64_t)kNumSMs * 6;                                            \
         e = launch_pdl(router_loss_grad_kernel<L, V>, dim3((unsigned)blocks), dim3(rloss::kThreads),                 \
                        sizeof(float) * G * 4 * V * L, stream, logits, idx, m, n, k, off, nseq, mask, fn, (double)alpha, \
                        (double)alpha_seq, (double)z_coef, counts, tokens, dloss, dgate, renorm, dlogits);            \
