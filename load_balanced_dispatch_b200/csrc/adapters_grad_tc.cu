@@ -41,7 +41,7 @@ __device__ __forceinline__ void split3(float v, __nv_bfloat16 (&p)[3]) {
     p[2] = __float2bfloat16_rn(r1 - __bfloat162float(p[1]));
 }
 
-// CTA c takes the row blocks (kRows grouped positions) c nb / grid .. (c + 1) nb / grid - 1. A group's
+// CTA c takes the row blocks (kRows grouped positions) c nb / ctas .. (c + 1) nb / ctas - 1. A group's
 // part of dB in CTA c goes to slot c + g: unique, since each next slot advances the CTA or the group.
 // LPR lanes load a row of dh, NQ 16-byte pieces each. Thread (te, tj) owns dB[NE te + a][NJ tj + b]; du has four
 // threads a row, each a quarter of the padded rank.
@@ -64,13 +64,14 @@ adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hi
     pdl_trigger();
     pdl_wait();
     const int nb = plan.goff[na + 1] / kRows;
-    const int b0 = (int)((int64_t)blockIdx.x * nb / gridDim.x), b1 = (int)((int64_t)(blockIdx.x + 1) * nb / gridDim.x);
+    const int ctas = min((int)gridDim.x, nb), c = (int)blockIdx.x;  // every CTA below `ctas` has a block
+    const int b0 = c < ctas ? (int)((int64_t)c * nb / ctas) : 0, b1 = c < ctas ? (int)((int64_t)(c + 1) * nb / ctas) : 0;
     const bool vec = (n & 3) == 0, uvec = (r & 3) == 0;
     float acc[NE][NJ];
     int g = -1;
     auto flush = [&]() {
         if (g < 0 || g >= na) return;
-        float* out = slots + ((int64_t)blockIdx.x + g) * n * r;
+        float* out = slots + ((int64_t)c + g) * n * r;
 #pragma unroll
         for (int a = 0; a < NE; ++a)
 #pragma unroll
@@ -105,18 +106,18 @@ adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hi
 #pragma unroll
         for (int i = 0; i < PASSES; ++i)
 #pragma unroll
-            for (int c = 0; c < NQ; ++c) {
-                const int e = 4 * (lcol + LPR * c);
-                v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < NQ; ++w) {
+                const int e = 4 * (lcol + LPR * w);
+                v[i][w] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (rows[i] >= 0) {
                     const float* src = dh + (int64_t)rows[i] * n + e;
                     if (vec) {
-                        if (e < n) v[i][c] = *reinterpret_cast<const float4*>(src);
+                        if (e < n) v[i][w] = *reinterpret_cast<const float4*>(src);
                     } else {
-                        if (e < n) v[i][c].x = src[0];
-                        if (e + 1 < n) v[i][c].y = src[1];
-                        if (e + 2 < n) v[i][c].z = src[2];
-                        if (e + 3 < n) v[i][c].w = src[3];
+                        if (e < n) v[i][w].x = src[0];
+                        if (e + 1 < n) v[i][w].y = src[1];
+                        if (e + 2 < n) v[i][w].z = src[2];
+                        if (e + 3 < n) v[i][w].w = src[3];
                     }
                 }
             }
@@ -239,17 +240,13 @@ adapters_fold_kernel(const float* __restrict__ slots, int n, int r, int d, int n
         for (int64_t i = i0; i < (int64_t)r * d; i += step) da[(int64_t)g * r * d + i] = 0.f;
         return;
     }
-    // the CTA of block b: the last c with c nb / grid <= b
-    auto cta = [&](int b) { return (int)((((int64_t)b + 1) * kGrid + nb - 1) / nb) - 1; };
+    // the CTA of block b: the last c with c nb / ctas <= b
+    const int ctas = min(kGrid, nb);
+    const int cf = (int)((((int64_t)b0 + 1) * ctas + nb - 1) / nb) - 1, cl = (int)(((int64_t)b1 * ctas + nb - 1) / nb) - 1;
     for (int i = i0; i < per; i += step) {
         float t = 0.f;
-        if (nb >= kGrid) {  // every CTA has blocks: those of the group follow one another
-            const int cf = cta(b0), cl = cta(b1 - 1);
-#pragma unroll 4
-            for (int c = cf; c <= cl; ++c) t += slots[((int64_t)c + g) * per + i];
-        } else {            // a CTA has one block at most
-            for (int b = b0; b < b1; ++b) t += slots[((int64_t)cta(b) + g) * per + i];
-        }
+#pragma unroll 8
+        for (int c = cf; c <= cl; ++c) t += slots[((int64_t)c + g) * per + i];
         db[(int64_t)g * per + i] = scale[g] * t;
     }
 }
@@ -511,7 +508,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
 
 // ---------------------------------------------------------------- contraction over rows
 namespace rct {
-constexpr int kThreads = 384, kDrain = 4, kMinRun = 4, BD = 256, BK = adp::kPad;
+constexpr int kThreads = 384, kDrain = 4, BD = 256, BK = adp::kPad;
 }
 
 struct RctShared {
@@ -570,7 +567,7 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
     volatile int* abort_flag = &sh->abort_flag;
     const int ndt = (d + BD - 1) / BD, nct = (ncols + C - 1) / C, U = ndt * nct;
     const int64_t total = (int64_t)(plan.goff[one ? na + 1 : na] / BK) * U;
-    int64_t ctas = total / kMinRun;
+    int64_t ctas = total / kLeastRun;  // the units' lengths differ: cut wherever it falls
     ctas = ctas < 1 ? 1 : (ctas > gridDim.x ? gridDim.x : ctas);
     const int64_t c = blockIdx.x;
     const int64_t lo = c < ctas ? c * total / ctas : total, hi = c < ctas ? (c + 1) * total / ctas : total;
@@ -723,10 +720,10 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
             }
             bool finish = true;
             if (kb0 != 0 || kb1 != u.nkb) {
-                float* mp = part + (2 * c + (kb0 == 0 ? 1 : 0)) * (int64_t)C * BD + row;
+                float4* mp = reinterpret_cast<float4*>(part) + (2 * c + (kb0 == 0 ? 1 : 0)) * (int64_t)C / 4 * BD + row;
                 if (ok && mine) {
 #pragma unroll
-                    for (int j = 0; j < C; ++j) __stcg(mp + (int64_t)j * BD, acc[j]);
+                    for (int j = 0; j < C; j += 4) __stcg(mp + (int64_t)(j / 4) * BD, make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
                 }
                 __threadfence();
                 ptx::named_barrier(1, 256);
@@ -742,9 +739,13 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
                     if (mine) {
                         for (int64_t cc = cf; cc <= cl; ++cc) {
                             const int64_t at = cc * total / ctas;  // where the CTA's run begins
-                            const float* op = part + (2 * cc + (at <= u.u0 ? 1 : 0)) * (int64_t)C * BD + row;
+                            const float4* op = reinterpret_cast<const float4*>(part) + (2 * cc + (at <= u.u0 ? 1 : 0)) * (int64_t)C / 4 * BD + row;
 #pragma unroll
-                            for (int j = 0; j < C; ++j) acc[j] = __fadd_rn(acc[j], __ldcg(op + (int64_t)j * BD));
+                            for (int j = 0; j < C; j += 4) {
+                                const float4 t = __ldcg(op + (int64_t)(j / 4) * BD);
+                                acc[j] = __fadd_rn(acc[j], t.x); acc[j + 1] = __fadd_rn(acc[j + 1], t.y);
+                                acc[j + 2] = __fadd_rn(acc[j + 2], t.z); acc[j + 3] = __fadd_rn(acc[j + 3], t.w);
+                            }
                         }
                     }
                 }

@@ -22,8 +22,17 @@ namespace moe {
 namespace atc {
 constexpr int BM = 256, BK = 64, kThreads = 384, kDrain = 4;
 constexpr int A_BYTES = BM * BK * 2;
-constexpr int kMinRun = 4;  // K blocks per CTA at least: shorter runs spend their time on partial sums
 }  // namespace atc
+
+// CTAs that share a line of `units` x nkb K blocks: every SM where there are units enough; else a whole number of
+// CTAs per unit, each with at least kLeastRun K blocks (shorter runs spend their time on the partial sums).
+constexpr int kLeastRun = 16;
+__device__ __forceinline__ int64_t line_ctas(int64_t units, int nkb) {
+    if (units >= (int64_t)gridDim.x || units == 0) return gridDim.x;
+    int64_t f = gridDim.x / units;
+    if (f > nkb / kLeastRun) f = nkb / kLeastRun;
+    return units * (f < 1 ? 1 : f);
+}
 
 struct AtcShared {
     uint64_t full[4], empty[4], tfull, tempty;
@@ -45,7 +54,7 @@ struct AtcTile {
     static constexpr int B_BYTES = (3 * NP + RP) * 128;
     static constexpr int STAGE = atc::A_BYTES + B_BYTES;
     static constexpr int STAGES = STAGE <= 65536 ? 3 : 2;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + (size_t)NP * RP * 4 + sizeof(AtcShared);
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + (size_t)NP * RP * 4 + 8 * 32 * 17 * 4 + sizeof(AtcShared);
     static_assert(2 * ACOLS <= 512, "both halves' accumulators fit the TMEM");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -74,7 +83,8 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* sB = reinterpret_cast<float*>(smem + STAGES * T::STAGE);  // [NP][RP] of B_a
-    AtcShared* sh = reinterpret_cast<AtcShared*>(sB + NP * RP);
+    float* stgs = sB + NP * RP;                                     // 8 warps x [32][17]
+    AtcShared* sh = reinterpret_cast<AtcShared*>(stgs + 8 * 32 * 17);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nkb = (d + BK - 1) / BK;
 
@@ -100,8 +110,7 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
 
     const int groups = na + 1;
     const int64_t total = (int64_t)plan.tstart[groups] * nct * nkb;
-    int64_t ctas = total / kMinRun;
-    ctas = ctas < 1 ? 1 : (ctas > gridDim.x ? gridDim.x : ctas);
+    const int64_t ctas = line_ctas(total / nkb, nkb);
     const int64_t c = blockIdx.x;
     const int64_t lo = c < ctas ? c * total / ctas : total, hi = c < ctas ? (c + 1) * total / ctas : total;
 
@@ -224,6 +233,7 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const int row = half * 128 + quad * 32 + lane;  // of the tile
         const int et = tid - 128;                       // 0 .. 255
+        float* stg = stgs + (warp - 4) * 32 * 17;
         const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * ACOLS);
         uint32_t tphase = 0;
         bool ok = true;
@@ -277,13 +287,15 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
             bool finish = true;
             if (kb0 != 0 || kb1 != nkb) {
                 // a part of the unit: leave the sums, and finish it if every other part is there already
-                float* mp = part + (2 * c + (kb0 == 0 ? 1 : 0)) * (int64_t)(NP + RP) * BM + row;
-                if (ok && mine) {
+                // [column / 4][row][4]: 16-byte accesses, a warp's rows beside one another
+                float4* mp = reinterpret_cast<float4*>(part) + (2 * c + (kb0 == 0 ? 1 : 0)) * (int64_t)(NP + RP) / 4 * BM + row;
+                if (ok && row < cnt) {
 #pragma unroll
-                    for (int j = 0; j < NP; ++j) __stcg(mp + (int64_t)j * BM, acc[j]);
+                    for (int j = 0; j < NP; j += 4) __stcg(mp + (int64_t)(j / 4) * BM, make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
                     if (ad) {
 #pragma unroll
-                        for (int j = 0; j < RP; ++j) __stcg(mp + (int64_t)(NP + j) * BM, u[j]);
+                        for (int j = 0; j < RP; j += 4)
+                            __stcg(mp + (int64_t)((NP + j) / 4) * BM, make_float4(u[j], u[j + 1], u[j + 2], u[j + 3]));
                     }
                 }
                 __threadfence();
@@ -299,15 +311,23 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                     for (int j = 0; j < NP; ++j) acc[j] = 0.f;
 #pragma unroll
                     for (int j = 0; j < RP; ++j) u[j] = 0.f;
-                    if (mine) {
+                    if (row < cnt) {
                         for (int64_t cc = cf; cc <= cl; ++cc) {
                             const int64_t at = cc * total / ctas;  // where the CTA's run begins
-                            const float* op = part + (2 * cc + (at <= u0 ? 1 : 0)) * (int64_t)(NP + RP) * BM + row;
+                            const float4* op = reinterpret_cast<const float4*>(part) + (2 * cc + (at <= u0 ? 1 : 0)) * (int64_t)(NP + RP) / 4 * BM + row;
 #pragma unroll
-                            for (int j = 0; j < NP; ++j) acc[j] = __fadd_rn(acc[j], __ldcg(op + (int64_t)j * BM));
+                            for (int j = 0; j < NP; j += 4) {
+                                const float4 t = __ldcg(op + (int64_t)(j / 4) * BM);
+                                acc[j] = __fadd_rn(acc[j], t.x); acc[j + 1] = __fadd_rn(acc[j + 1], t.y);
+                                acc[j + 2] = __fadd_rn(acc[j + 2], t.z); acc[j + 3] = __fadd_rn(acc[j + 3], t.w);
+                            }
                             if (ad) {
 #pragma unroll
-                                for (int j = 0; j < RP; ++j) u[j] = __fadd_rn(u[j], __ldcg(op + (int64_t)(NP + j) * BM));
+                                for (int j = 0; j < RP; j += 4) {
+                                    const float4 t = __ldcg(op + (int64_t)((NP + j) / 4) * BM);
+                                    u[j] = __fadd_rn(u[j], t.x); u[j + 1] = __fadd_rn(u[j + 1], t.y);
+                                    u[j + 2] = __fadd_rn(u[j + 2], t.z); u[j + 3] = __fadd_rn(u[j + 3], t.w);
+                                }
                             }
                         }
                     }
@@ -322,48 +342,62 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                     }
                     ptx::named_barrier(1, 256);
                 }
-                if (ok && row < cnt) {
-                    const int64_t out = plan.perm[p0 + row];
+                // 16 columns at a time through the warp's staging rows: rolled loops over the columns (unrolled in
+                // full, the NP x RP products are 30 to 80 KB of code that every launch fetches anew) and stores of 64-byte pieces
+                if (ok && half * 128 + quad * 32 < cnt) {  // the same for the warp
+                    const int32_t out = row < cnt ? plan.perm[p0 + row] : -1;
+                    float* mine = stg + lane * 17;
+                    auto store16 = [&](float* dst, int width, int col) {
+                        __syncwarp();
+#pragma unroll 4
+                        for (int i = 0; i < 16; ++i) {
+                            const int q = 2 * i + (lane >> 4), cc = col + (lane & 15);
+                            const int32_t to = __shfl_sync(0xffffffffu, out, q);
+                            if (to >= 0 && cc < width) dst[(int64_t)to * width + cc] = stg[q * 17 + (lane & 15)];
+                        }
+                        __syncwarp();
+                    };
                     if (hidden && ct == 0) {
-                        float* hp = hidden + out * r;
-                        if ((r & 3) == 0) {
 #pragma unroll
-                            for (int j = 0; j < RP; j += 4)
-                                if (j < r) *reinterpret_cast<float4*>(hp + j) = make_float4(u[j], u[j + 1], u[j + 2], u[j + 3]);
-                        } else {
+                        for (int q = 0; q < RP; q += 16) {
+                            if (q < r) {
 #pragma unroll
-                            for (int j = 0; j < RP; ++j)
-                                if (j < r) hp[j] = u[j];
+                                for (int j = 0; j < 16; ++j) mine[j] = u[q + j];
+                                store16(hidden, r, q);
+                            }
                         }
                     }
                     if (ad) {
                         const float s = scale[g];
 #pragma unroll
                         for (int j = 0; j < RP; ++j) u[j] *= s;
-#pragma unroll
-                        for (int e = 0; e < NP; ++e) {
-                            float t0 = 0.f, t1 = 0.f;
-#pragma unroll
-                            for (int q = 0; q < RP; q += 4) {
-                                const float4 b4 = *reinterpret_cast<const float4*>(sB + e * RP + q);
-                                t0 = fmaf(u[q], b4.x, t0);
-                                t1 = fmaf(u[q + 1], b4.y, t1);
-                                t0 = fmaf(u[q + 2], b4.z, t0);
-                                t1 = fmaf(u[q + 3], b4.w, t1);
-                            }
-                            acc[e] += t0 + t1;
-                        }
                     }
-                    float* lp = logits + out * n + ct * NP;
-                    if ((n & 3) == 0) {
 #pragma unroll
-                        for (int e = 0; e < NP; e += 4)
-                            if (ct * NP + e < n)
-                                *reinterpret_cast<float4*>(lp + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-                    } else {
+                    for (int e0 = 0; e0 < NP; e0 += 16) {
+                        if (ct * NP + e0 < n) {
 #pragma unroll
-                        for (int e = 0; e < NP; ++e)
-                            if (ct * NP + e < n) lp[e] = acc[e];
+                            for (int j = 0; j < 16; ++j) mine[j] = acc[e0 + j];
+                            if (ad) {
+#pragma unroll 4
+                                for (int j = 0; j < 16; ++j) {
+                                    float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+                                    for (int q8 = 0; q8 < RP; q8 += 16) {
+                                        if (q8 >= r) continue;
+#pragma unroll
+                                        for (int q = q8; q < q8 + 16; q += 4) {
+                                            const float4 b4 = *reinterpret_cast<const float4*>(sB + (e0 + j) * RP + q);
+                                            t0 = fmaf(u[q], b4.x, t0);
+                                            t1 = fmaf(u[q + 1], b4.y, t1);
+                                            t0 = fmaf(u[q + 2], b4.z, t0);
+                                            t1 = fmaf(u[q + 3], b4.w, t1);
+                                        }
+                                    }
+                                    mine[j] += t0 + t1;
+                                }
+                            }
+                            store16(logits, n, ct * NP + e0);
+                        }
                     }
                 }
             }
