@@ -329,107 +329,116 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
         return cnt < 0 ? 0 : min(cnt, 128 * MH);
     };
 
+    const uint32_t leader = lane == 0 ? 1u : 0u;
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, aphase = 0;
-            int64_t held = -1;
-            int g = 0, p0 = 0, cnt = 0;
-            bool ok = true;
-            for (int64_t u = lo; ok && u < hi; ++u) {
-                const int64_t tile = u / ndc;
-                const int d0 = (int)(u - tile * ndc) * ND;
-                if (tile != held) {
-                    held = tile;
-                    cnt = rows_of(tile, g, p0);
-                    if (cnt > 0) {
-                        const int halves = cnt > 128 ? 2 : 1;
-                        ok = ptx::mbar_wait(&sh->aempty, aphase ^ 1u, abort_flag);
-                        if (!ok) break;
-                        aphase ^= 1u;
-                        ptx::mbar_expect_tx(&sh->afull, (uint32_t)(halves * 16384 * (2 * NC + (g < na ? T::DU_CHUNKS : 0))));
-                        for (int h = 0; h < halves; ++h) {
-                            for (int p = 0; p < 2; ++p)
-                                for (int c = 0; c < NC; ++c)
-                                    ptx::tma_load_3d(sa + ((p * NC + c) * MH + h) * 16384, &map_dh, &sh->afull, 64 * c, p0 + 128 * h, p);
-                            if (g < na)
-                                for (int c = 0; c < T::DU_CHUNKS; ++c)
-                                    ptx::tma_load_2d(su + (c * MH + h) * 16384, &map_du, &sh->afull, 64 * c, p0 + 128 * h);
+        int stage = 0;
+        uint32_t phase = 0, aphase = 0;
+        int64_t held = -1;
+        int g = 0, p0 = 0, cnt = 0;
+        bool ok = true;
+        for (int64_t u = lo; ok && u < hi; ++u) {
+            const int64_t tile = u / ndc;
+            const int d0 = (int)(u - tile * ndc) * ND;
+            if (tile != held) {
+                held = tile;
+                cnt = rows_of(tile, g, p0);
+                if (cnt > 0) {
+                    const int halves = cnt > 128 ? 2 : 1;
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->aempty, aphase ^ 1u, abort_flag));
+                    if (!ok) break;
+                    aphase ^= 1u;
+                    if (leader) ptx::mbar_expect_tx(&sh->afull, (uint32_t)(halves * 16384 * (2 * NC + (g < na ? T::DU_CHUNKS : 0))));
+                    __syncwarp();
+                    for (int h = 0; h < halves; ++h) {
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)
+#pragma unroll
+                            for (int c = 0; c < NC; ++c)
+                                ptx::tma_load_3d_if(leader, sa + ((p * NC + c) * MH + h) * 16384, &map_dh, &sh->afull, 64 * c, p0 + 128 * h, p);
+                        if (g < na) {
+#pragma unroll
+                            for (int c = 0; c < T::DU_CHUNKS; ++c)
+                                ptx::tma_load_2d_if(leader, su + (c * MH + h) * 16384, &map_du, &sh->afull, 64 * c, p0 + 128 * h);
                         }
                     }
                 }
-                if (cnt == 0) continue;
-                for (int c = 0; c < NC + (g < na ? 1 : 0); ++c) {
-                    ok = ptx::mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag);
-                    if (!ok) break;
-                    uint8_t* st = ring + stage * T::STAGE;
-                    if (c < NC) {
-                        ptx::mbar_expect_tx(&sh->full[stage], 2 * ND * 128);
-                        for (int p = 0; p < 2; ++p) ptx::tma_load_3d(st + p * ND * 128, &map_w, &sh->full[stage], 64 * c, d0, p);
-                    } else {
-                        ptx::mbar_expect_tx(&sh->full[stage], ND / 64 * RP * 128);
-                        for (int q = 0; q < ND / 64; ++q)
-                            ptx::tma_load_3d(st + q * RP * 128, &map_a, &sh->full[stage], d0 + 64 * q, 0, g);
-                    }
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            }
+            if (cnt == 0) continue;
+            for (int c = 0; c < NC + (g < na ? 1 : 0); ++c) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag));
+                if (!ok) break;
+                uint8_t* st = ring + stage * T::STAGE;
+                if (leader) ptx::mbar_expect_tx(&sh->full[stage], c < NC ? 2 * ND * 128 : ND / 64 * RP * 128);
+                __syncwarp();
+                if (c < NC) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) ptx::tma_load_3d_if(leader, st + p * ND * 128, &map_w, &sh->full[stage], 64 * c, d0, p);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < ND / 64; ++q)
+                        ptx::tma_load_3d_if(leader, st + q * RP * 128, &map_a, &sh->full[stage], d0 + 64 * q, 0, g);
                 }
+                if (++stage == kStages) { stage = 0; phase ^= 1u; }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, ND);
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, aphase = 0, bphase = 0;
-            int64_t held = -1;
-            int g = 0, p0 = 0, cnt = 0;
-            bool ok = true;
-            for (int64_t u = lo; ok && u < hi; ++u) {
-                const int64_t tile = u / ndc;
-                if (tile != held) {
-                    if (held >= 0 && cnt > 0) ptx::umma_commit(&sh->aempty);  // the tile before has been read
-                    held = tile;
-                    cnt = rows_of(tile, g, p0);
-                    if (cnt > 0) {
-                        ok = ptx::mbar_wait(&sh->afull, aphase, abort_flag);
-                        if (!ok) break;
-                        aphase ^= 1u;
-                    }
-                }
-                if (cnt == 0) continue;
-                const int halves = cnt > 128 ? 2 : 1;
-                ok = ptx::mbar_wait(&sh->tempty[buf], bphase ^ 1u, abort_flag);
-                if (!ok) break;
-                for (int c = 0; c < NC + (g < na ? 1 : 0); ++c) {
-                    ok = ptx::mbar_wait(&sh->full[stage], phase, abort_flag);
+        constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, ND);
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, aphase = 0, bphase = 0;
+        int64_t held = -1;
+        int g = 0, p0 = 0, cnt = 0;
+        bool ok = true;
+        for (int64_t u = lo; ok && u < hi; ++u) {
+            const int64_t tile = u / ndc;
+            if (tile != held) {
+                if (held >= 0 && cnt > 0) ptx::umma_commit_if(leader, &sh->aempty);  // the tile before has been read
+                held = tile;
+                cnt = rows_of(tile, g, p0);
+                if (cnt > 0) {
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->afull, aphase, abort_flag));
                     if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t st = ptx::smem_u32(ring + stage * T::STAGE);
-                    for (int h = 0; h < halves; ++h) {
-                        const uint32_t acc = tmem + (uint32_t)((buf * MH + h) * ND);
-                        if (c < NC) {
-                            const int steps = min(4, (n - 64 * c + 15) / 16);
-                            const uint64_t ahi = ptx::sw128_kmajor_desc(ptx::smem_u32(sa + (c * MH + h) * 16384));
-                            const uint64_t alo = ptx::sw128_kmajor_desc(ptx::smem_u32(sa + ((NC + c) * MH + h) * 16384));
-                            const uint64_t bhi = ptx::sw128_kmajor_desc(st), blo = ptx::sw128_kmajor_desc(st + ND * 128);
-                            for (int k = 0; k < steps; ++k) ptx::umma_bf16(acc, ahi + 2 * k, bhi + 2 * k, idesc, (c | k) != 0);
-                            for (int k = 0; k < steps; ++k) ptx::umma_bf16(acc, alo + 2 * k, bhi + 2 * k, idesc, 1u);
-                            for (int k = 0; k < steps; ++k) ptx::umma_bf16(acc, ahi + 2 * k, blo + 2 * k, idesc, 1u);
-                        } else {
-                            const int steps = (r + 15) / 16;
-                            const uint32_t ua = ptx::smem_u32(su + h * 16384);
-                            const uint64_t uhi = ptx::sw128_kmajor_desc(ua);
-                            const uint64_t ulo = RP == 32 ? uhi + 4 : ptx::sw128_kmajor_desc(ua + MH * 16384);
-                            const uint64_t bd = sw128_mnmajor_desc(st, RP * 128);
-                            for (int k = 0; k < steps; ++k) ptx::umma_bf16(acc, uhi + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
-                            for (int k = 0; k < steps; ++k) ptx::umma_bf16(acc, ulo + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
-                        }
-                    }
-                    ptx::umma_commit(&sh->empty[stage]);
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    aphase ^= 1u;
                 }
-                ptx::umma_commit(&sh->tfull[buf]);
-                if (++buf == 2) { buf = 0; bphase ^= 1u; }
             }
+            if (cnt == 0) continue;
+            const int halves = cnt > 128 ? 2 : 1;
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->tempty[buf], bphase ^ 1u, abort_flag));
+            if (!ok) break;
+            for (int c = 0; c < NC + (g < na ? 1 : 0); ++c) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->full[stage], phase, abort_flag));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t st = ptx::smem_u32(ring + stage * T::STAGE);
+                for (int h = 0; h < halves; ++h) {
+                    const uint32_t acc = tmem + (uint32_t)((buf * MH + h) * ND);
+                    if (c < NC) {  // columns behind n are zero on both sides
+                        const uint64_t ahi = ptx::sw128_kmajor_desc(ptx::smem_u32(sa + (c * MH + h) * 16384));
+                        const uint64_t alo = ptx::sw128_kmajor_desc(ptx::smem_u32(sa + ((NC + c) * MH + h) * 16384));
+                        const uint64_t bhi = ptx::sw128_kmajor_desc(st), blo = ptx::sw128_kmajor_desc(st + ND * 128);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) ptx::umma_bf16_if(leader, acc, ahi + 2 * k, bhi + 2 * k, idesc, (c | k) != 0);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) ptx::umma_bf16_if(leader, acc, alo + 2 * k, bhi + 2 * k, idesc, 1u);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) ptx::umma_bf16_if(leader, acc, ahi + 2 * k, blo + 2 * k, idesc, 1u);
+                    } else {
+                        const uint32_t ua = ptx::smem_u32(su + h * 16384);
+                        const uint64_t uhi = ptx::sw128_kmajor_desc(ua);
+                        const uint64_t ulo = RP == 32 ? uhi + 4 : ptx::sw128_kmajor_desc(ua + MH * 16384);
+                        const uint64_t bd = sw128_mnmajor_desc(st, RP * 128);
+#pragma unroll
+                        for (int k = 0; k < RP / 16; ++k)
+                            if (16 * k < r) {
+                                ptx::umma_bf16_if(leader, acc, uhi + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
+                                ptx::umma_bf16_if(leader, acc, ulo + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
+                            }
+                    }
+                }
+                ptx::umma_commit_if(leader, &sh->empty[stage]);
+                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            }
+            ptx::umma_commit_if(leader, &sh->tfull[buf]);
+            if (++buf == 2) { buf = 0; bphase ^= 1u; }
         }
     } else if (warp >= 4) {
         const int quad = warp & 3, grp = (warp - 4) >> 2;
@@ -595,6 +604,7 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
         return u;
     };
 
+    const uint32_t leader = lane == 0 ? 1u : 0u;
     if (warp < 4) {
         ptx::regs_less<72>();
         if (warp != 1) {
@@ -605,18 +615,23 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
                 const Unit u = unit_at(pos);
                 const int kb0 = (int)(pos - u.u0), kb1 = (int)min((int64_t)u.nkb, kb0 + (hi - pos));
                 const int slab = warp & 1, quad = lane & 7, chunk = lane >> 3;  // warps 2, 3: slab 0, 1
-                for (int kb = kb0; kb < kb1; ++kb) {
+                // the block's first and last row of each slab and, in the gather warps, four rows a lane; the next
+                // block's are on their way while this one is issued
+                auto look = [&](int kb, int4& e, int4& v) {
+                    const int32_t* q = plan.perm + (int64_t)(u.blk0 + kb) * BK;
+                    e = make_int4(q[0], q[31], q[32], q[63]);
+                    if (warp >= 2) v = *reinterpret_cast<const int4*>(q + 32 * slab + 4 * quad);
+                };
+                int4 edge, four = make_int4(0, 0, 0, 0), edge1, four1 = four;
+                look(kb0, edge, four);
+                for (int kb = kb0; kb < kb1; ++kb, edge = edge1, four = four1) {
                     const int p0 = (u.blk0 + kb) * BK;
-                    const int first0 = plan.perm[p0], last0 = plan.perm[p0 + 31];
-                    const int first1 = plan.perm[p0 + 32], last1 = plan.perm[p0 + 63];
-                    const bool run0 = last0 >= 0 && last0 - first0 == 31, run1 = last1 >= 0 && last1 - first1 == 31;
+                    if (kb + 1 < kb1) look(kb + 1, edge1, four1);
+                    const int first0 = edge.x, first1 = edge.z;
+                    const bool run0 = edge.y >= 0 && edge.y - first0 == 31, run1 = edge.w >= 0 && edge.w - first1 == 31;
                     const bool gather = warp >= 2 && !(slab == 0 ? run0 : run1);
-                    int rid[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int v = gather ? plan.perm[p0 + 32 * slab + 4 * quad + q] : 0;
-                        rid[q] = v < 0 ? first0 : v;
-                    }
+                    const int rid[4] = {four.x < 0 ? first0 : four.x, four.y < 0 ? first0 : four.y,
+                                        four.z < 0 ? first0 : four.z, four.w < 0 ? first0 : four.w};
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag));
                     if (!ok) break;
                     uint8_t* st = smem + stage * T::STAGE;
@@ -628,13 +643,13 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
                                                            : (gather ? 16384 : 0));
                     __syncwarp();
                     if (warp == 0) {
-                        if (lane < 8 && ((lane & 1) == 0 ? run0 : run1))  // chunk lane / 2, slab lane & 1
-                            ptx::tma_load_2d(st + (lane >> 1) * BK * 128 + (lane & 1) * 4096, &map_x, bar,
-                                             u.dt * BD + 64 * (lane >> 1), (lane & 1) == 0 ? first0 : first1);
-                        if (lane >= 8 && lane < 8 + T::CHUNKS) {
-                            const int q = lane - 8;
-                            // dh: a plane per part; du: the parts beside one another
-                            ptx::tma_load_3d(st + T::X_BYTES + q * BK * 128, &map_p, bar, one ? C * u.ct : 64 * q, p0, one ? q : 0);
+#pragma unroll
+                        for (int q = 0; q < T::CHUNKS; ++q)  // dh: a plane per part; du: the parts beside one another
+                            ptx::tma_load_3d_if(leader, st + T::X_BYTES + q * BK * 128, &map_p, bar, one ? C * u.ct : 64 * q, p0, one ? q : 0);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (run0) ptx::tma_load_2d_if(leader, st + q * BK * 128, &map_x, bar, u.dt * BD + 64 * q, first0);
+                            if (run1) ptx::tma_load_2d_if(leader, st + q * BK * 128 + 4096, &map_x, bar, u.dt * BD + 64 * q, first1);
                         }
                     } else if (gather) {
                         tma_gather4(st + chunk * BK * 128 + slab * 4096 + quad * 512, &map_g, bar, u.dt * BD + 64 * chunk, rid[0],
@@ -645,39 +660,37 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
                 pos += kb1 - kb0;
             }
         } else {
-            if (lane == 0) {
-                constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, ACOLS) | kIdescAMn | kIdescBMn;
-                int stage = 0;
-                uint32_t phase = 0, tphase = 0;
-                bool ok = true;
-                for (int64_t pos = lo; ok && pos < hi;) {
-                    const Unit u = unit_at(pos);
-                    const int kb0 = (int)(pos - u.u0), kb1 = (int)min((int64_t)u.nkb, kb0 + (hi - pos));
-                    const int halves = d - u.dt * BD > 128 ? 2 : 1;
-                    for (int kb = kb0; kb < kb1; ++kb) {
-                        const int in = (kb - kb0) % kDrain;
-                        if (in == 0) {
-                            ok = ptx::mbar_wait(&sh->tempty, tphase ^ 1u, abort_flag);
-                            if (!ok) break;
-                        }
-                        ok = ptx::mbar_wait(&sh->full[stage], phase, abort_flag);
+            constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, ACOLS) | kIdescAMn | kIdescBMn;
+            int stage = 0;
+            uint32_t phase = 0, tphase = 0;
+            bool ok = true;
+            for (int64_t pos = lo; ok && pos < hi;) {
+                const Unit u = unit_at(pos);
+                const int kb0 = (int)(pos - u.u0), kb1 = (int)min((int64_t)u.nkb, kb0 + (hi - pos));
+                const int halves = d - u.dt * BD > 128 ? 2 : 1;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    const int in = (kb - kb0) % kDrain;
+                    if (in == 0) {
+                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->tempty, tphase ^ 1u, abort_flag));
                         if (!ok) break;
-                        ptx::tc_fence_after();
-                        const uint32_t st = ptx::smem_u32(smem + stage * T::STAGE);
-                        const uint64_t bdesc = sw128_mnmajor_desc(st + T::X_BYTES, BK * 128);
-                        for (int h = 0; h < halves; ++h) {
-                            const uint64_t adesc = sw128_mnmajor_desc(st + h * 2 * BK * 128, BK * 128);
-#pragma unroll
-                            for (int kk = 0; kk < BK / 16; ++kk)
-                                ptx::umma_bf16(tmem + (uint32_t)(h * ACOLS), adesc + 128 * kk, bdesc + 128 * kk, idesc,
-                                               (in != 0 || kk != 0) ? 1u : 0u);
-                        }
-                        ptx::umma_commit(&sh->empty[stage]);
-                        if (in == kDrain - 1 || kb == kb1 - 1) { ptx::umma_commit(&sh->tfull); tphase ^= 1u; }
-                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     }
-                    pos += kb1 - kb0;
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->full[stage], phase, abort_flag));
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t st = ptx::smem_u32(smem + stage * T::STAGE);
+                    const uint64_t bdesc = sw128_mnmajor_desc(st + T::X_BYTES, BK * 128);
+                    for (int h = 0; h < halves; ++h) {
+                        const uint64_t adesc = sw128_mnmajor_desc(st + h * 2 * BK * 128, BK * 128);
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            ptx::umma_bf16_if(leader, tmem + (uint32_t)(h * ACOLS), adesc + 128 * kk, bdesc + 128 * kk, idesc,
+                                           (in != 0 || kk != 0) ? 1u : 0u);
+                    }
+                    ptx::umma_commit_if(leader, &sh->empty[stage]);
+                    if (in == kDrain - 1 || kb == kb1 - 1) { ptx::umma_commit_if(leader, &sh->tfull); tphase ^= 1u; }
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
+                pos += kb1 - kb0;
             }
         }
     } else {

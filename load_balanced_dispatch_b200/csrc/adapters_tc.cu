@@ -125,6 +125,7 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
     };
 
     // 384 x 168 registers at launch = 128 x 72 + 256 x 216: the drain keeps a row's sums in registers
+    const uint32_t leader = lane == 0 ? 1u : 0u;
     if (warp < 4) {
         ptx::regs_less<72>();
         if (warp != 1) {
@@ -164,14 +165,13 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                     __syncwarp();
                     if (warp == 0) {
                         // B rows: fused [W0 W1 W2 A], else [W0 A W1 W2]
-                        if (lane >= 8 && lane < 11) {
-                            const int p = lane - 8;
-                            const int row = p * NP + (!T::FUSED && p > 0 ? RP : 0);
-                            ptx::tma_load_3d(sb + row * 128, &map_w, bar, kb * BK, ct * NP, p);
-                        }
-                        if (lane == 11 && ad)
-                            ptx::tma_load_3d(sb + (T::FUSED ? 3 * NP : NP) * 128, &map_a, bar, kb * BK, 0, g);
-                        if (lane < 8 && run) ptx::tma_load_2d(st + lane * 4096, &map_x, bar, kb * BK, first);
+#pragma unroll
+                        for (int p = 0; p < 3; ++p)
+                            ptx::tma_load_3d_if(leader, sb + (p * NP + (!T::FUSED && p > 0 ? RP : 0)) * 128, &map_w, bar, kb * BK, ct * NP, p);
+                        if (ad) ptx::tma_load_3d_if(leader, sb + (T::FUSED ? 3 * NP : NP) * 128, &map_a, bar, kb * BK, 0, g);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (boxes >> q & 1u) ptx::tma_load_2d_if(leader, st + q * 4096, &map_x, bar, kb * BK, __shfl_sync(0xffffffffu, first, q));
                     } else if (gather) {
                         tma_gather4(st + quad * 128, &map_g, bar, kb * BK, rid[0], rid[1], rid[2], rid[3]);
                     }
@@ -180,52 +180,50 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                 pos += kb1 - kb0;
             }
         } else {
-            if (lane == 0) {
-                int stage = 0;
-                uint32_t phase = 0, tphase = 0;
-                bool ok = true;
-                for (int64_t pos = lo; ok && pos < hi;) {
-                    const int64_t unit = pos / nkb;
-                    const int kb0 = (int)(pos - unit * nkb);
-                    const int kb1 = (int)min((int64_t)nkb, kb0 + (hi - pos));
-                    int ct, g, p0;
-                    const int cnt = rows_of(unit, ct, g, p0);
-                    const int halves = cnt > 128 ? 2 : 1, wide = g < na ? RP : 0;
-                    const uint32_t idesc = ptx::idesc_bf16_f32(128, (T::FUSED ? 3 * NP : NP) + wide);
-                    const uint32_t idesc_w = ptx::idesc_bf16_f32(128, NP);
-                    for (int kb = kb0; kb < kb1; ++kb) {
-                        const int in = (kb - kb0) % kDrain;
-                        if (in == 0) {
-                            ok = ptx::mbar_wait(&sh->tempty, tphase ^ 1u, abort_flag);
-                            if (!ok) break;
-                        }
-                        ok = ptx::mbar_wait(&sh->full[stage], phase, abort_flag);
+            int stage = 0;
+            uint32_t phase = 0, tphase = 0;
+            bool ok = true;
+            for (int64_t pos = lo; ok && pos < hi;) {
+                const int64_t unit = pos / nkb;
+                const int kb0 = (int)(pos - unit * nkb);
+                const int kb1 = (int)min((int64_t)nkb, kb0 + (hi - pos));
+                int ct, g, p0;
+                const int cnt = rows_of(unit, ct, g, p0);
+                const int halves = cnt > 128 ? 2 : 1, wide = g < na ? RP : 0;
+                const uint32_t idesc = ptx::idesc_bf16_f32(128, (T::FUSED ? 3 * NP : NP) + wide);
+                const uint32_t idesc_w = ptx::idesc_bf16_f32(128, NP);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    const int in = (kb - kb0) % kDrain;
+                    if (in == 0) {
+                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->tempty, tphase ^ 1u, abort_flag));
                         if (!ok) break;
-                        ptx::tc_fence_after();
-                        const uint32_t sa = ptx::smem_u32(smem + stage * T::STAGE);
-                        const uint64_t bdesc = ptx::sw128_kmajor_desc(sa + A_BYTES);
-                        for (int h = 0; h < halves; ++h) {
-                            const uint64_t adesc = ptx::sw128_kmajor_desc(sa + h * 16384);
-                            const uint32_t acc = tmem + (uint32_t)(h * ACOLS);
+                    }
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->full[stage], phase, abort_flag));
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t sa = ptx::smem_u32(smem + stage * T::STAGE);
+                    const uint64_t bdesc = ptx::sw128_kmajor_desc(sa + A_BYTES);
+                    for (int h = 0; h < halves; ++h) {
+                        const uint64_t adesc = ptx::sw128_kmajor_desc(sa + h * 16384);
+                        const uint32_t acc = tmem + (uint32_t)(h * ACOLS);
 #pragma unroll
-                            for (int kk = 0; kk < BK / 16; ++kk)
-                                ptx::umma_bf16(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc, (in != 0 || kk != 0) ? 1u : 0u);
-                            if (!T::FUSED) {
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            ptx::umma_bf16_if(leader, acc, adesc + 2 * kk, bdesc + 2 * kk, idesc, (in != 0 || kk != 0) ? 1u : 0u);
+                        if (!T::FUSED) {
 #pragma unroll
-                                for (int p = 1; p < 3; ++p) {
-                                    const uint64_t wdesc = ptx::sw128_kmajor_desc(sa + A_BYTES + (p * NP + RP) * 128);
+                            for (int p = 1; p < 3; ++p) {
+                                const uint64_t wdesc = ptx::sw128_kmajor_desc(sa + A_BYTES + (p * NP + RP) * 128);
 #pragma unroll
-                                    for (int kk = 0; kk < BK / 16; ++kk)
-                                        ptx::umma_bf16(acc, adesc + 2 * kk, wdesc + 2 * kk, idesc_w, 1u);
-                                }
+                                for (int kk = 0; kk < BK / 16; ++kk)
+                                    ptx::umma_bf16_if(leader, acc, adesc + 2 * kk, wdesc + 2 * kk, idesc_w, 1u);
                             }
                         }
-                        ptx::umma_commit(&sh->empty[stage]);
-                        if (in == kDrain - 1 || kb == kb1 - 1) { ptx::umma_commit(&sh->tfull); tphase ^= 1u; }
-                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     }
-                    pos += kb1 - kb0;
+                    ptx::umma_commit_if(leader, &sh->empty[stage]);
+                    if (in == kDrain - 1 || kb == kb1 - 1) { ptx::umma_commit_if(leader, &sh->tfull); tphase ^= 1u; }
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
+                pos += kb1 - kb0;
             }
         }
     } else {

@@ -240,6 +240,48 @@ __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.
 template <int R>
 __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
+// The same operations for a warp that walks its loop together, executed by the lane whose `on` is set (one lane).
+// Inside a one-lane branch the descriptors and coordinates, which the instruction takes from uniform registers, are
+// moved there one by one for every instruction; in code that the whole warp runs they are computed there.
+__device__ __forceinline__ void umma_bf16_if(uint32_t on, uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t on, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_if(uint32_t on, void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                               int c1) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_if(uint32_t on, void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                               int c1, int c2) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];\n\t}" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(on)
+        : "memory");
+}
+
 // ---- thread-block clusters: rank, distributed shared memory, cluster-wide barrier
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;
