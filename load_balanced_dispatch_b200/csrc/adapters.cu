@@ -249,104 +249,216 @@ static cudaError_t launch_adapter_prep(const int32_t* idx, int64_t m, int na, co
     return cudaLaunchKernelEx(&cfg, adapter_prep_kernel, idx, m, na, p, tickets, ntickets, x, cluster);
 }
 
-// ---- forward: R rows per CTA, thread (column, row group); 32 input columns at a time through
-// shared memory. The products of 32 columns are summed first and then added to the row's sum, so the
-// rounding errors grow with the number of blocks, not of columns.
-template <int NPAD>
-__global__ void __launch_bounds__(adp::kThreads)
-adapters_rows_kernel(const float* __restrict__ x, const float* __restrict__ w_r, const float* __restrict__ a,
-                     const float* __restrict__ bmat, const int32_t* __restrict__ idx, const float* __restrict__ scale,
-                     int64_t m, int d, int n, int r, int na, float* __restrict__ logits, float* __restrict__ hidden) {
-    using namespace adp;
-    constexpr int KC = 32, RG = kThreads / NPAD, R = RG > 16 ? RG : 16, RPT = R / RG, V = Vec16<float>::N;
-    __shared__ float xs[R][KC + 1];
-    __shared__ float ws[KC][NPAD + 1];
-    __shared__ float us[R][kMaxRank + 1];
+// ---- forward of four rows by a cluster of 1 to 8 CTAs that shares out the columns of d: all fp32 batches, and bf16
+// batches of few rows (adapters_run.cu has the rule). In a CTA, eight warps read its slice of W_r once for the four
+// rows (a thread: four columns, every KL-th row of the slice) and eight form u (a warp: four products at a time, lanes
+// along d; A_a is read once for the rows when they share it). These are other warps (512 threads) while all clusters
+// surely run at once (and W_r is not the larger part), and the same ones (256 threads, three CTAs per SM) for more rows: 8 against 11 us for 32 rows of 2048
+// columns, but 102 against 54 us for 4096 rows of 512. The slices' sums meet in distributed
+// shared memory, where each CTA finishes a part of the columns. Nothing is grouped and one launch does all, so a step
+// of few rows is bound by the latency of that chain;
+// a large batch by the reads of A_a from L2, 1.5 us per 2^20 of m d r.
+constexpr int kFewRows = 4, kFewSlice = 512;  // rows of a cluster; columns of d in shared memory at a time
+
+// Sums of four values over the warp, in six shuffles: lane l gets the sum of t[l / 8].
+__device__ __forceinline__ float warp_sum4(const float (&t)[4], int lane) {
+    float a = lane & 16 ? t[2] : t[0], b = lane & 16 ? t[3] : t[1];
+    a += __shfl_xor_sync(0xffffffffu, lane & 16 ? t[0] : t[2], 16);
+    b += __shfl_xor_sync(0xffffffffu, lane & 16 ? t[1] : t[3], 16);
+    float c = (lane & 8 ? b : a) + __shfl_xor_sync(0xffffffffu, lane & 8 ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    return c;
+}
+
+template <typename T, int TH>
+__global__ void __launch_bounds__(TH, TH == 256 ? 3 : 1)
+adapters_few_kernel(const T* __restrict__ x, const float* __restrict__ w_r, const T* __restrict__ a,
+                    const T* __restrict__ bmat, const int32_t* __restrict__ idx, const float* __restrict__ scale,
+                    int64_t m, int d, int n, int r, int na, int cluster, float* __restrict__ logits,
+                    float* __restrict__ hidden) {
+    constexpr int V = Vec16<T>::N, kThreads = TH, WT = 256, W = 8;
+    __shared__ float xs[kFewRows][kFewSlice];
+    __shared__ float4 red[kFewRows][WT];                          // a thread's four columns of each row
+    __shared__ float sl[kFewRows][kMaxExperts], su[kFewRows][kMaxRank];  // this slice's sums (read by the cluster)
+    __shared__ float us[kFewRows][kMaxRank];                      // s u, complete
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int col = tid % NPAD, rg = tid / NPAD;
+    const int uw = TH == 512 ? wid - W : wid;  // which of the warps that form u
     pdl_trigger();
     pdl_wait();
-    const int64_t row0 = (int64_t)blockIdx.x * R;
-    float acc[RPT];
+    const int rank = (int)blockIdx.x % cluster;
+    const int64_t row0 = (int64_t)(blockIdx.x / cluster) * kFewRows;
+    const int rows = (int)min((int64_t)kFewRows, m - row0);
+    const int per = (d / V + cluster - 1) / cluster * V;          // columns of a slice, whole 16-byte pieces
+    const int k0 = min(rank * per, d), k1 = min(k0 + per, d);
+    int ad[kFewRows];
 #pragma unroll
-    for (int q = 0; q < RPT; ++q) acc[q] = 0.f;
-    for (int k0 = 0; k0 < d; k0 += KC) {
-        for (int i = tid; i < R * KC; i += kThreads) {
-            const int rr = i / KC, kk = i % KC;
-            xs[rr][kk] = (row0 + rr < m && k0 + kk < d) ? x[(row0 + rr) * d + k0 + kk] : 0.f;
+    for (int q = 0; q < kFewRows; ++q) ad[q] = q < rows ? idx[row0 + q] : -1;
+#pragma unroll
+    for (int q = 0; q < kFewRows; ++q)
+        if (ad[q] < -1 || ad[q] >= na) {
+            if (tid == 0 && rank == 0) record_error(kErrAdapterIndex);
+            ad[q] = -1;
         }
-        for (int i = tid; i < KC * n; i += kThreads) {
-            const int kk = i / n, j = i % n;
-            ws[kk][j] = k0 + kk < d ? w_r[(int64_t)(k0 + kk) * n + j] : 0.f;
+    const bool shared = ad[0] >= 0 && ad[0] == ad[1] && ad[0] == ad[2] && ad[0] == ad[3];
+    const int cq = (n + 3) / 4, kl = WT / cq, col = tid % cq, kg = tid / cq;
+    const bool vec = (n & 3) == 0, mine = tid < WT && kg < kl;
+    float4 acc[kFewRows];
+#pragma unroll
+    for (int q = 0; q < kFewRows; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = tid; i < kFewRows * r; i += kThreads) su[i / r][i % r] = 0.f;
+    for (int c0 = k0; c0 < k1; c0 += kFewSlice) {
+        const int len = min(kFewSlice, k1 - c0);
+        __syncthreads();
+        for (int i = tid; i < kFewRows * (kFewSlice / V); i += kThreads) {
+            const int q = i / (kFewSlice / V), c = i % (kFewSlice / V) * V;
+            if (c >= len) continue;
+            float v[V];
+#pragma unroll
+            for (int u = 0; u < V; ++u) v[u] = 0.f;
+            if (q < rows) Vec16<T>::load(x + (row0 + q) * d + c0 + c, v);
+#pragma unroll
+            for (int u = 0; u < V; ++u) xs[q][c + u] = v[u];
         }
         __syncthreads();
-        float blk[RPT];
-#pragma unroll
-        for (int q = 0; q < RPT; ++q) blk[q] = 0.f;
-        if (col < n) {
+        if (mine) {
+            const float* wp = w_r + (int64_t)c0 * n + 4 * col;
 #pragma unroll 8
-            for (int kk = 0; kk < KC; ++kk) {
-                const float wv = ws[kk][col];
+            for (int k = kg; k < len; k += kl) {
+                float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float* src = wp + (int64_t)k * n;
+                if (vec) {
+                    w = *reinterpret_cast<const float4*>(src);
+                } else {
+                    w.x = src[0];
+                    if (4 * col + 1 < n) w.y = src[1];
+                    if (4 * col + 2 < n) w.z = src[2];
+                    if (4 * col + 3 < n) w.w = src[3];
+                }
 #pragma unroll
-                for (int q = 0; q < RPT; ++q) blk[q] = fmaf(xs[rg + RG * q][kk], wv, blk[q]);
+                for (int q = 0; q < kFewRows; ++q) {
+                    const float xv = xs[q][k];
+                    acc[q].x = fmaf(xv, w.x, acc[q].x);
+                    acc[q].y = fmaf(xv, w.y, acc[q].y);
+                    acc[q].z = fmaf(xv, w.z, acc[q].z);
+                    acc[q].w = fmaf(xv, w.w, acc[q].w);
+                }
             }
         }
+        if (uw >= 0 && shared) {  // a rank at a time, its product with each row
+#pragma unroll 4
+            for (int j = uw; j < r; j += W) {
+                const T* ap = a + ((int64_t)ad[0] * r + j) * d + c0;
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int c = lane * V; c < len; c += 32 * V) {
+                    float v[V];
+                    Vec16<T>::load(ap + c, v);
 #pragma unroll
-        for (int q = 0; q < RPT; ++q) acc[q] += blk[q];
-        __syncthreads();
+                    for (int p = 0; p < 4; ++p)
+#pragma unroll
+                        for (int u = 0; u < V; ++u) t[p] = fmaf(xs[p][c + u], v[u], t[p]);
+                }
+                const float sum = warp_sum4(t, lane);
+                if ((lane & 7) == 0) su[lane >> 3][j] += sum;
+            }
+        } else if (uw >= 0) {  // products i = (row, rank), a warp takes i0, i0 + W, ...: four at a time
+            for (int i0 = uw; i0 < kFewRows * r; i0 += 4 * W) {
+                float t[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int i = i0 + p * W, q = i / r, j = i - q * r;
+                    t[p] = 0.f;
+                    const int own = q == 0 ? ad[0] : q == 1 ? ad[1] : q == 2 ? ad[2] : ad[3];
+                    if (i < kFewRows * r && own >= 0) {
+                        const T* ap = a + ((int64_t)own * r + j) * d + c0;
+                        for (int c = lane * V; c < len; c += 32 * V) {
+                            float v[V];
+                            Vec16<T>::load(ap + c, v);
+#pragma unroll
+                            for (int u = 0; u < V; ++u) t[p] = fmaf(xs[q][c + u], v[u], t[p]);
+                        }
+                    }
+                }
+                const float sum = warp_sum4(t, lane);
+                const int i = i0 + (lane >> 3) * W;
+                if ((lane & 7) == 0 && i < kFewRows * r) su[i / r][i % r] += sum;
+            }
+        }
     }
-    // u: a warp per row, four of the adapter's rows at a time, lanes along d
-    for (int rr = wid; rr < R; rr += kThreads / 32) {
-        const int64_t row = row0 + rr;
-        if (row >= m) break;
-        int ad = idx[row];
-        if (ad < -1 || ad >= na) { if (lane == 0) record_error(kErrAdapterIndex); ad = -1; }
-        if (ad < 0) {
-            for (int j = lane; j < r; j += 32) { us[rr][j] = 0.f; if (hidden) hidden[row * r + j] = 0.f; }
-            continue;
-        }
-        const float sc = scale[ad];
-        for (int j0 = 0; j0 < r; j0 += 4) {
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int c = lane * V; c < d; c += 32 * V) {
-                float xv[V], av[V];
-                Vec16<float>::load(x + row * d + c, xv);
+    if (mine) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (j0 + q >= r) continue;
-                    Vec16<float>::load(a + ((int64_t)ad * r + j0 + q) * d + c, av);
-                    float t = 0.f;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) t = fmaf(xv[i], av[i], t);
-                    s[q] += t;
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float t = warp_sum(s[q]);
-                if (lane == q && j0 + q < r) {
-                    us[rr][j0 + q] = sc * t;
-                    if (hidden) hidden[row * r + j0 + q] = t;
-                }
-            }
-        }
+        for (int q = 0; q < kFewRows; ++q) red[q][kg * cq + col] = acc[q];
     }
     __syncthreads();
-    if (col < n) {
-#pragma unroll
-        for (int q = 0; q < RPT; ++q) {
-            const int rr = rg + RG * q;
-            const int64_t row = row0 + rr;
-            if (row >= m) continue;
-            const int ad = idx[row];
-            float t = 0.f;
-            if (ad >= 0 && ad < na) {
-                const float* bp = bmat + ((int64_t)ad * n + col) * r;
-                for (int j = 0; j < r; ++j) t = fmaf(us[rr][j], bp[j], t);
-            }
-            logits[row * n + col] = acc[q] + t;
+    for (int i = tid; i < kFewRows * cq; i += kThreads) {
+        const int q = i / cq, c = i % cq;
+        float4 t = red[q][c];
+#pragma unroll 8
+        for (int k = 1; k < kl; ++k) {
+            const float4 v = red[q][k * cq + c];
+            t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
         }
+        *reinterpret_cast<float4*>(&sl[q][4 * c]) = t;
     }
+    if (cluster > 1) ptx::cluster_sync(); else __syncthreads();
+    for (int i = tid; i < rows * r; i += kThreads) {
+        const int q = i / r, j = i % r;
+        float t = 0.f;
+        for (int k = 0; k < cluster; ++k)
+            t += cluster > 1 ? ptx::ld_cluster_f32(ptx::mapa_shared(ptx::smem_u32(&su[q][j]), k)) : su[q][j];
+        if (rank == 0 && hidden) hidden[(row0 + q) * r + j] = t;
+        us[q][j] = ad[q] >= 0 ? scale[ad[q]] * t : 0.f;
+    }
+    __syncthreads();
+    for (int i = rank * kThreads + tid; i < rows * n; i += cluster * kThreads) {
+        const int q = i / n, e = i % n;
+        float t = 0.f;
+        for (int k = 0; k < cluster; ++k)
+            t += cluster > 1 ? ptx::ld_cluster_f32(ptx::mapa_shared(ptx::smem_u32(&sl[q][e]), k)) : sl[q][e];
+        if (ad[q] >= 0) {
+            const T* bp = bmat + ((int64_t)ad[q] * n + e) * r;
+            float v = 0.f;
+            if (r % V == 0) {
+#pragma unroll 2
+                for (int j = 0; j < r; j += V) {
+                    float bv[V];
+                    Vec16<T>::load(bp + j, bv);
+#pragma unroll
+                    for (int u = 0; u < V; ++u) v = fmaf(us[q][j + u], bv[u], v);
+                }
+            } else {
+#pragma unroll 8
+                for (int j = 0; j < r; ++j) v = fmaf(us[q][j], Elem<T>::load(bp + j), v);
+            }
+            t += v;
+        }
+        logits[(row0 + q) * n + e] = t;
+    }
+    if (cluster > 1) ptx::cluster_sync();  // nobody leaves while its sums may still be read
+}
+
+template <typename T>
+static cudaError_t launch_adapters_few(const T* x, const float* w_r, const T* a, const T* b, const int32_t* idx,
+                                       const float* scale, int64_t m, int d, int n, int r, int na, float* logits,
+                                       float* hidden, cudaStream_t stream) {
+    int cluster = 1;
+    while (cluster < 8 && d / cluster > 256) cluster *= 2;  // slices of 256 columns or so
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((m + kFewRows - 1) / kFewRows * cluster));
+    const bool at_once = cfg.gridDim.x <= (unsigned)kNumSMs * 3 / 4 && n <= 128;
+    cfg.blockDim = dim3(at_once ? 512 : 256);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, at_once ? adapters_few_kernel<T, 512> : adapters_few_kernel<T, 256>, x, w_r, a, b, idx, scale, m, d, n, r, na, cluster, logits,
+                              hidden);
 }
 
 // ---- dx: 16 rows x 128 columns of d per CTA

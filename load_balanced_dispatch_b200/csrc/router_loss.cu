@@ -70,6 +70,13 @@ __device__ __forceinline__ int seq_of_row(const int32_t* __restrict__ off, int n
     return lo - 1;
 }
 
+// The same by the whole block, in one read where the offsets are few (a binary search is a chain of reads).
+__device__ __forceinline__ int seq_of_row_block(const int32_t* __restrict__ off, int nseq, int64_t r) {
+    if (nseq >= rloss::kThreads) return seq_of_row(off, nseq, r);
+    const int tid = threadIdx.x;
+    return __syncthreads_count(tid <= nseq && (int64_t)off[min(tid, nseq)] <= r) - 1;
+}
+
 // The 4 V logits that lane `sub` of the row's L lanes owns: columns 4 (sub + L v) .. + 3, v < V.
 // Columns past n read as -inf (no score, no weight).
 template <int L, int V>
@@ -131,14 +138,14 @@ __device__ __forceinline__ float row_softmax(float (&h)[4 * V]) {
 __device__ __forceinline__ float logistic(float h) { return 1.f / (1.f + expf(-h)); }
 
 template <int L, int V>
-__global__ void __launch_bounds__(rloss::kThreads)
+__global__ void __launch_bounds__(rloss::kThreads, 3)
 router_loss_chunk_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx, int64_t m, int n, int k,
                          const int32_t* __restrict__ off, int nseq, const uint8_t* __restrict__ mask, int fn,
                          int want_z, RouterLossWs w) {
     using namespace rloss;
     constexpr int RW = 32 / L;                      // rows a warp holds
     constexpr int GROUPS = (kThreads / 32) * RW;    // rows the CTA holds at a time
-    constexpr int U = GROUPS >= 64 ? 1 : 4;         // rows in flight per lane group
+    constexpr int U = GROUPS >= 64 ? 1 : V == 2 ? 2 : 4;  // rows in flight per lane group
     constexpr int FS = 4 * V * L + 1;
     extern __shared__ double fold[];                // [GROUPS][FS] a row group's sums
     __shared__ double tot_p[kMaxExperts];
@@ -155,9 +162,10 @@ router_loss_chunk_kernel(const float* __restrict__ logits, const int32_t* __rest
     double z = 0.0;
     int total = 0;
     for (int64_t at = r0; at < r1;) {
-        const int s = seq_of_row(off, nseq, at);
+        const int s = seq_of_row_block(off, nseq, at);
         if (s >= nseq) break;                                        // behind the last sequence
-        const int64_t next = min((int64_t)off[s + 1], r1);           // > at: off[s + 1] is the first offset above it
+        // off[s + 1] is the first offset above `at`; offsets that do not ascend (an error) may not be: step on all the same
+        const int64_t next = max(at + 1, min((int64_t)off[s + 1], r1));
         if (s < 0) { at = next; continue; }                          // before the first
         if (tid < n) cnt[tid] = 0;
         if (tid == 0) ntok = 0;
@@ -215,6 +223,7 @@ router_loss_chunk_kernel(const float* __restrict__ logits, const int32_t* __rest
 #pragma unroll
             for (int q = 0; q < 4 * V; ++q) {
                 float t = h[0][q];
+                if constexpr (U == 2) t = h[0][q] + h[1][q];
                 if constexpr (U == 4) t = (h[0][q] + h[1][q]) + (h[2][q] + h[3][q]);
                 acc[q] += (double)t;
             }
@@ -283,8 +292,11 @@ router_loss_fold_kernel(int64_t m, int n, int k, const int32_t* __restrict__ off
     const int32_t* ptok = whole ? w.ttok : w.ptok + s;
     double a = 0.0;
     int cn = 0, tk = 0;
+    const int ec = min(e, n - 1);
+#pragma unroll 8
     for (int64_t c = c0 + wid; c < c1; c += W) {
-        if (e < n) { a += psum[c * n + e]; cn += pcnt[c * n + e]; }
+        a += psum[c * n + ec];
+        cn += pcnt[c * n + ec];
         tk += ptok[c];
     }
     ps[wid][lane] = a;
@@ -364,7 +376,7 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
     using namespace rloss;
     constexpr int RW = 32 / L, GROUPS = (kThreads / 32) * RW, U = 2;
     constexpr int CW = 4 * V * L;
-    extern __shared__ float scat[];  // [GROUPS][CW]: a row's logits for its picks, then what the gates add to each column
+    extern __shared__ float bufs[];  // [GROUPS][U][2][CW]: a row's logits for its picks; what the gates add to each column
     __shared__ int s_full;
     const int tid = threadIdx.x, lane = tid & 31, sub = lane % L, grp = (tid >> 5) * RW + lane / L;
     const bool vec = (n & 3) == 0;
@@ -378,15 +390,15 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
         if (full) atomicAdd(&s_full, full);
         __syncthreads();
     }
-    float* mine = scat + grp * CW;
+    float* mine = bufs + grp * U * 2 * CW;
     if (dgate)
-        for (int j = sub; j < CW; j += L) mine[j] = 0.f;
+        for (int j = sub; j < U * 2 * CW; j += L) mine[j] = 0.f;
     __syncwarp();
     const double up = dloss ? (double)*dloss : 1.0;
     const int T = max(tokens[nseq], 1);
     const bool soft = fn == MOE_SOFTMAX;
     const float cz = (float)(2.0 * z_coef * up / T);
-    const bool chosen = soft && renorm && k > 1;  // gate = softmax over the picks
+    const bool chosen = soft && renorm && k > 1 && dgate;  // gate = softmax over the picks
     const double full = alpha_seq != 0.0 ? (double)max(s_full, 1) : 1.0;
     // a table row's part of g for the owned columns: coef / T * (count n - k T) / (k T), or coef / T * count n / (k T)
     auto table = [&](const int32_t* row, int64_t t, double coef, float (&g)[4 * V]) {
@@ -407,32 +419,31 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
     const int64_t r0 = ((int64_t)blockIdx.x * GROUPS + grp) * per, r1 = min(r0 + per, m);
     int seq = -2;
     int64_t seq_end = -1;  // the rows below it that follow the current one belong to `seq`
-    // every lane of a warp runs the same number of rounds: the row's lanes reduce together
+    // every lane of a warp runs the same number of rounds (the row's lanes reduce together), and the rows of a round
+    // go through each step together, so that one's shuffles hide the other's
     for (int64_t i = 0; i < per; i += U) {
-        float h[U][4 * V], dg[U];
+        float h[U][4 * V], g[U][4 * V], dg[U], x0[U];
         int pick[U];
         bool live[U];
-        bool ok[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + i + u;
-            ok[u] = i + u < per && r < r1 && (!mask || mask[r]);
+            live[u] = i + u < per && r < r1 && (!mask || mask[r]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + i + u;
 #pragma unroll
             for (int q = 0; q < 4 * V; ++q) h[u][q] = -INFINITY;
-            if (ok[u]) load_row<L, V>(logits + r * n, n, vec, sub, h[u]);
-            const bool has = ok[u] && dgate && sub < k;
+            if (live[u]) load_row<L, V>(logits + r * n, n, vec, sub, h[u]);
+            const bool has = live[u] && dgate && sub < k;
             pick[u] = has ? idx[r * k + sub] : -1;
             dg[u] = has ? dgate[r * k + sub] : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + i + u;
-            const bool in = i + u < per && r < r1;
-            if (in && r >= seq_end) {
+            if (i + u < per && r < r1 && r >= seq_end) {
                 seq = seq_of_row(off, nseq, r);
                 seq_end = seq >= nseq ? m : (int64_t)off[seq + 1];
                 if (alpha_seq != 0.0 && seq >= 0 && seq < nseq) {
@@ -441,123 +452,155 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
                     for (int q = 0; q < 4 * V; ++q) gt[q] += gG[q];
                 }
             }
-            live[u] = ok[u] && seq >= 0 && seq < nseq;
-            float add[4 * V];
+            live[u] = live[u] && seq >= 0 && seq < nseq;
+            if (!live[u] || pick[u] < 0 || pick[u] >= n) pick[u] = -1;
 #pragma unroll
-            for (int q = 0; q < 4 * V; ++q) add[q] = 0.f;
-            if (dgate) {
-                if (chosen) {
-                    // q_r = softmax over the picks' logits; dL/dh = q_r (dg_r - sum q dg)
+            for (int q = 0; q < 4 * V; ++q) g[u][q] = gt[q];
+        }
+        // the picks: their logits, or what their gates add to g
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        *reinterpret_cast<float4*>(mine + 4 * (sub + L * v)) =
-                            make_float4(h[u][4 * v], h[u][4 * v + 1], h[u][4 * v + 2], h[u][4 * v + 3]);
-                    __syncwarp();
-                    const int e0 = live[u] && pick[u] >= 0 && pick[u] < n ? pick[u] : -1;
-                    const float x0 = e0 >= 0 ? mine[e0] : -INFINITY;
-                    float top = x0;
-                    for (int t = sub + L; t < k; t += L) {
-                        const int e = live[u] ? idx[r * k + t] : -1;
-                        if (e >= 0 && e < n) top = fmaxf(top, mine[e]);
-                    }
-                    top = lanes_max<L>(top);
-                    if (top == -INFINITY) top = 0.f;  // no pick has a score: every weight is 0
-                    const float w0 = expf(x0 - top);
-                    float sum = w0, dot = w0 * dg[u];
-                    for (int t = sub + L; t < k; t += L) {
-                        const int e = live[u] ? idx[r * k + t] : -1;
-                        if (e >= 0 && e < n) {
-                            const float x = expf(mine[e] - top);
-                            sum += x;
-                            dot = fmaf(x, dgate[r * k + t], dot);
-                        }
-                    }
-                    sum = lanes_sum<L>(sum);
-                    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-                    dot = lanes_sum<L>(dot) * inv;
-                    // further picks (k > L): their terms wait in registers of the second pass over the row's logits
-                    float keep[4 * V];
+        for (int u = 0; u < U; ++u) {
+            float* logit = mine + u * 2 * CW;
+            float* add = logit + CW;
+            if (chosen) {
 #pragma unroll
-                    for (int q = 0; q < 4 * V; ++q) keep[q] = 0.f;
-                    if (k > L) {
-                        // column j's term, from the picks that name it: each lane looks at every pick
-                        for (int t = 0; t < k; ++t) {
-                            const int e = live[u] ? idx[r * k + t] : -1;
-#pragma unroll
-                            for (int v = 0; v < V; ++v)
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    if (e == 4 * (sub + L * v) + q && e < n)
-                                        keep[4 * v + q] += expf(h[u][4 * v + q] - top) * inv * (dgate[r * k + t] - dot);
-                        }
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        *reinterpret_cast<float4*>(mine + 4 * (sub + L * v)) = make_float4(keep[4 * v], keep[4 * v + 1], keep[4 * v + 2], keep[4 * v + 3]);
-                    __syncwarp();
-                    if (k <= L && e0 >= 0) atomicAdd(&mine[e0], w0 * inv * (dg[u] - dot));
-                } else {
-                    if (live[u] && pick[u] >= 0 && pick[u] < n) atomicAdd(&mine[pick[u]], dg[u]);
-                    for (int t = sub + L; t < k; t += L) {
-                        const int e = live[u] ? idx[r * k + t] : -1;
-                        if (e >= 0 && e < n) atomicAdd(&mine[e], dgate[r * k + t]);
-                    }
-                }
-                __syncwarp();
-                // read the row's columns and clear them for the next row
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float4* at = reinterpret_cast<float4*>(mine + 4 * (sub + L * v));
-                    const float4 t = *at;
-                    *at = make_float4(0.f, 0.f, 0.f, 0.f);
-                    add[4 * v] = t.x; add[4 * v + 1] = t.y; add[4 * v + 2] = t.z; add[4 * v + 3] = t.w;
-                }
-                __syncwarp();
-            }
-            float out[4 * V];
-            if (soft) {
-                const float lse = row_softmax<L, V>(h[u]);  // h is the score now
-                float c = 0.f;
-                float g[4 * V];
-#pragma unroll
-                for (int q = 0; q < 4 * V; ++q) {
-                    g[q] = gt[q] + (chosen ? 0.f : add[q]);
-                    c = fmaf(h[u][q], g[q], c);
-                }
-                c = lanes_sum<L>(c);
-#pragma unroll
-                for (int q = 0; q < 4 * V; ++q) out[q] = fmaf(h[u][q], g[q] - c + cz * lse, chosen ? add[q] : 0.f);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4 * V; ++q)  // 1 - rho from its own exponential: exact for large h
-                    out[q] = (gt[q] + add[q]) * logistic(h[u][q]) * logistic(-h[u][q]);
-                if (cz != 0.f) {
-                    const float lse = row_softmax<L, V>(h[u]);
-#pragma unroll
-                    for (int q = 0; q < 4 * V; ++q) out[q] = fmaf(cz * lse, h[u][q], out[q]);
-                }
-            }
-            if (in) {
-                float* row = dlogits + r * n;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int j = 4 * (sub + L * v);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (!live[u]) out[4 * v + q] = 0.f;
-                    if (vec) {
-                        if (j < n)
-                            *reinterpret_cast<float4*>(row + j) =
-                                make_float4(out[4 * v], out[4 * v + 1], out[4 * v + 2], out[4 * v + 3]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (j + q < n) row[j + q] = out[4 * v + q];
-                    }
+                for (int v = 0; v < V; ++v)
+                    *reinterpret_cast<float4*>(logit + 4 * (sub + L * v)) = make_float4(h[u][4 * v], h[u][4 * v + 1], h[u][4 * v + 2], h[u][4 * v + 3]);
+            } else if (dgate) {
+                if (pick[u] >= 0) atomicAdd(&add[pick[u]], dg[u]);
+                for (int t = sub + L; t < k; t += L) {
+                    const int e = live[u] ? idx[(r0 + i + u) * k + t] : -1;
+                    if (e >= 0 && e < n) atomicAdd(&add[e], dgate[(r0 + i + u) * k + t]);
                 }
             }
         }
+        __syncwarp();
+        float top[U], ptop[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float* logit = mine + u * 2 * CW;
+            float* add = mine + u * 2 * CW + CW;
+            x0[u] = -INFINITY;
+            if (chosen) {
+                if (pick[u] >= 0) x0[u] = logit[pick[u]];
+            } else if (dgate) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float4* at = reinterpret_cast<float4*>(add + 4 * (sub + L * v));
+                    const float4 t = *at;
+                    *at = make_float4(0.f, 0.f, 0.f, 0.f);
+                    g[u][4 * v] += t.x; g[u][4 * v + 1] += t.y; g[u][4 * v + 2] += t.z; g[u][4 * v + 3] += t.w;
+                }
+            }
+            ptop[u] = x0[u];
+            if (chosen)
+                for (int t = sub + L; t < k; t += L) {
+                    const int e = live[u] ? idx[(r0 + i + u) * k + t] : -1;
+                    if (e >= 0 && e < n) ptop[u] = fmaxf(ptop[u], logit[e]);
+                }
+            top[u] = h[u][0];
+#pragma unroll
+            for (int q = 1; q < 4 * V; ++q) top[u] = fmaxf(top[u], h[u][q]);
+        }
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+                if (chosen) ptop[u] = fmaxf(ptop[u], __shfl_xor_sync(0xffffffffu, ptop[u], o));
+            }
+        float s[U], eg[U], sq[U], dq[U], w0[U];
+        float e[U][4 * V];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            s[u] = eg[u] = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4 * V; ++q) {
+                // a row without scores: e = 0, but NaN stays
+                e[u][q] = top[u] == -INFINITY ? (h[u][q] == -INFINITY ? 0.f : h[u][q]) : expf(h[u][q] - top[u]);
+                s[u] += e[u][q];
+                eg[u] = fmaf(e[u][q], g[u][q], eg[u]);
+            }
+            if (ptop[u] == -INFINITY) ptop[u] = 0.f;  // no pick has a score: every weight is 0
+            w0[u] = chosen ? expf(x0[u] - ptop[u]) : 0.f;
+            sq[u] = w0[u];
+            dq[u] = w0[u] * dg[u];
+            if (chosen)
+                for (int t = sub + L; t < k; t += L) {
+                    const int p = live[u] ? idx[(r0 + i + u) * k + t] : -1;
+                    if (p >= 0 && p < n) {
+                        const float x = expf(mine[u * 2 * CW + p] - ptop[u]);
+                        sq[u] += x;
+                        dq[u] = fmaf(x, dgate[(r0 + i + u) * k + t], dq[u]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+                if (soft) eg[u] += __shfl_xor_sync(0xffffffffu, eg[u], o);
+                if (chosen) {
+                    sq[u] += __shfl_xor_sync(0xffffffffu, sq[u], o);
+                    dq[u] += __shfl_xor_sync(0xffffffffu, dq[u], o);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float inv = top[u] == -INFINITY ? 1.f : 1.f / s[u];
+            const float lse = top[u] == -INFINITY ? s[u] : top[u] + logf(s[u]);
+            if (soft) {
+                const float c = eg[u] * inv - cz * lse;
+#pragma unroll
+                for (int q = 0; q < 4 * V; ++q) e[u][q] *= inv * (g[u][q] - c);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4 * V; ++q) {  // 1 - rho from its own exponential: exact for large h
+                    const float z = cz != 0.f ? cz * lse * inv * e[u][q] : 0.f;
+                    e[u][q] = fmaf(g[u][q] * logistic(h[u][q]), logistic(-h[u][q]), z);
+                }
+            }
+            if (chosen) {  // dL/dh of a pick: q_r (dg_r - sum q dg)
+                const float iq = sq[u] != 0.f ? 1.f / sq[u] : 0.f, dot = dq[u] * iq;
+                float* add = mine + u * 2 * CW + CW;
+                if (pick[u] >= 0) atomicAdd(&add[pick[u]], w0[u] * iq * (dg[u] - dot));
+                for (int t = sub + L; t < k; t += L) {
+                    const int p = live[u] ? idx[(r0 + i + u) * k + t] : -1;
+                    if (p >= 0 && p < n)
+                        atomicAdd(&add[p], expf(mine[u * 2 * CW + p] - ptop[u]) * iq * (dgate[(r0 + i + u) * k + t] - dot));
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + i + u;
+            const bool in = i + u < per && r < r1;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int j = 4 * (sub + L * v);
+                float4 o = make_float4(e[u][4 * v], e[u][4 * v + 1], e[u][4 * v + 2], e[u][4 * v + 3]);
+                if (chosen) {
+                    float4* at = reinterpret_cast<float4*>(mine + u * 2 * CW + CW + j);
+                    const float4 t = *at;
+                    *at = make_float4(0.f, 0.f, 0.f, 0.f);
+                    o.x += t.x; o.y += t.y; o.z += t.z; o.w += t.w;
+                }
+                if (!live[u]) o = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!in) continue;
+                float* row = dlogits + r * n + j;
+                if (vec) {
+                    if (j < n) *reinterpret_cast<float4*>(row) = o;
+                } else {
+                    if (j < n) row[0] = o.x;
+                    if (j + 1 < n) row[1] = o.y;
+                    if (j + 2 < n) row[2] = o.z;
+                    if (j + 3 < n) row[3] = o.w;
+                }
+            }
+        }
+        __syncwarp();
     }
 }
 
@@ -606,11 +649,11 @@ cudaError_t launch_router_loss_grad(const float* logits, const int32_t* idx, int
     cudaError_t e = cudaSuccess;
 #define CALL(L, V)                                                                                                   \
     do {                                                                                                             \
-        constexpr int G = (rloss::kThreads / 32) * (32 / L);                                                         \
+        constexpr int G = (rloss::kThreads / 32) * (32 / L), most = kNumSMs * (V == 2 ? 2 : 4);                      \
         int64_t blocks = (m + G - 1) / G;                                                                            \
-        if (blocks > (int64_t)kNumSMs * 6) blocks = (int64_t)kNumSMs * 6;                                            \
+        if (blocks > most) blocks = most;  /* one wave */                                                            \
         e = launch_pdl(router_loss_grad_kernel<L, V>, dim3((unsigned)blocks), dim3(rloss::kThreads),                 \
-                       sizeof(float) * G * 4 * V * L, stream, logits, idx, m, n, k, off, nseq, mask, fn, (double)alpha, \
+                       sizeof(float) * G * 2 * 2 * 4 * V * L, stream, logits, idx, m, n, k, off, nseq, mask, fn, (double)alpha, \
                        (double)alpha_seq, (double)z_coef, counts, tokens, dloss, dgate, renorm, dlogits);            \
     } while (0)
     MOE_ROUTER_LOSS_DISPATCH(n, CALL);
