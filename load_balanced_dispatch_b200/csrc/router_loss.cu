@@ -26,6 +26,7 @@ namespace rloss {
 constexpr int kRows = 128;     // rows per CTA of the chunk pass
 constexpr int kThreads = 256;
 constexpr int kFoldCols = 32;  // experts per CTA of the fold
+constexpr int kFoldThreads = 512;
 }  // namespace rloss
 
 struct RouterLossWs {
@@ -111,6 +112,8 @@ __device__ __forceinline__ float lanes_max(float v) {
     return v;
 }
 
+// The exponentials are __expf (off by 2 + 1.2 |x| ulp, which is below 2^-18 where exp(x) is above 2^-24 of a row's
+// sum); expf made the passes wait for instruction issue, at 37 and 56 instructions a logit.
 // h_j <- exp(h_j - top) / sum, and the log-sum-exp of a row held by L lanes. A row whose logits are
 // all -inf has no scores: 0 throughout and lse = 0. NaN and +inf give NaN.
 template <int L, int V>
@@ -119,26 +122,21 @@ __device__ __forceinline__ float row_softmax(float (&h)[4 * V]) {
 #pragma unroll
     for (int q = 1; q < 4 * V; ++q) top = fmaxf(top, h[q]);
     top = lanes_max<L>(top);
+    if (top == -INFINITY) top = 0.f;
     float s = 0.f;
-    if (top == -INFINITY) {  // fmaxf passes over NaN: keep it in the sum
 #pragma unroll
-        for (int q = 0; q < 4 * V; ++q) { h[q] = h[q] == -INFINITY ? 0.f : h[q]; s += h[q]; }
-    } else {
-#pragma unroll
-        for (int q = 0; q < 4 * V; ++q) { h[q] = expf(h[q] - top); s += h[q]; }
-    }
+    for (int q = 0; q < 4 * V; ++q) { h[q] = __expf(h[q] - top); s += h[q]; }
     s = lanes_sum<L>(s);
-    if (top == -INFINITY) return s;
-    const float inv = 1.f / s;
+    const float inv = s == 0.f ? 0.f : 1.f / s;
 #pragma unroll
     for (int q = 0; q < 4 * V; ++q) h[q] *= inv;
-    return top + logf(s);
+    return s == 0.f ? 0.f : top + logf(s);
 }
 
-__device__ __forceinline__ float logistic(float h) { return 1.f / (1.f + expf(-h)); }
+__device__ __forceinline__ float logistic(float h) { return __fdividef(1.f, 1.f + __expf(-h)); }
 
 template <int L, int V>
-__global__ void __launch_bounds__(rloss::kThreads, 3)
+__global__ void __launch_bounds__(rloss::kThreads, 4)
 router_loss_chunk_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx, int64_t m, int n, int k,
                          const int32_t* __restrict__ off, int nseq, const uint8_t* __restrict__ mask, int fn,
                          int want_z, RouterLossWs w) {
@@ -251,26 +249,26 @@ router_loss_chunk_kernel(const float* __restrict__ logits, const int32_t* __rest
     if (sub == 0) zpart[grp] = z;
     if (tid < n) { w.tsum[c * n + tid] = tot_p[tid]; w.tcnt[c * n + tid] = tot_c[tid]; }
     __syncthreads();
-    if (tid == 0) {
+    if (tid < 32) {
         double t = 0.0;
-        for (int g = 0; g < GROUPS; ++g) t += zpart[g];
-        w.zsum[c] = t;
-        w.ttok[c] = total;
+        for (int g = tid; g < GROUPS; g += 32) t += zpart[g];
+        t = warp_sum_d(t);
+        if (tid == 0) { w.zsum[c] = t; w.ttok[c] = total; }
     }
 }
 
-// blockIdx.x = sequence (nseq: the whole batch), blockIdx.y = 32 experts; 8 rows of 32 lanes.
-__global__ void __launch_bounds__(rloss::kThreads)
+// blockIdx.x = sequence (nseq: the whole batch), blockIdx.y = 32 experts; a warp takes every 16th chunk.
+__global__ void __launch_bounds__(rloss::kFoldThreads)
 router_loss_fold_kernel(int64_t m, int n, int k, const int32_t* __restrict__ off, int nseq, double alpha,
                         double alpha_seq, double z_coef, float* __restrict__ loss, int32_t* __restrict__ counts,
                         int32_t* __restrict__ tokens, float* __restrict__ f, float* __restrict__ P, RouterLossWs w) {
     using namespace rloss;
-    constexpr int W = kThreads / 32;
+    constexpr int W = kFoldThreads / 32;
     __shared__ double ps[W][kFoldCols];
     __shared__ int cs[W][kFoldCols];
     __shared__ int ts[W];
-    __shared__ double red[kThreads];
-    __shared__ int redi[kThreads];
+    __shared__ double red[W], redz[W];
+    __shared__ int redi[W];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     pdl_trigger();
@@ -328,27 +326,23 @@ router_loss_fold_kernel(int64_t m, int n, int k, const int32_t* __restrict__ off
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    // the last CTA: the sequences' losses in order (thread t takes sequences t, t + 256, ...)
+    // the last CTA: the sequences' losses in order (thread t takes sequences t, t + 512, ...)
     const int ncb = gridDim.y;
     double seq = 0.0;
     int full = 0;
-    for (int q = tid; q < nseq; q += kThreads) {
+    for (int q = tid; q < nseq; q += kFoldThreads) {
         for (int b = 0; b < ncb; ++b) seq += __ldcg(w.part + (int64_t)q * ncb + b);
         full += __ldcg(tokens + q) > 0;
     }
     double z = 0.0;
-    for (int64_t c = tid; c < nch; c += kThreads) z += __ldcg(w.zsum + c);
-    red[tid] = seq;
-    redi[tid] = full;
+    for (int64_t c = tid; c < nch; c += kFoldThreads) z += __ldcg(w.zsum + c);
+    seq = warp_sum_d(seq);
+    z = warp_sum_d(z);
+    full = __reduce_add_sync(0xffffffffu, full);
+    if (lane == 0) { red[wid] = seq; redz[wid] = z; redi[wid] = full; }
     __syncthreads();
     if (tid == 0) {
-        for (int q = 1; q < kThreads; ++q) { seq += red[q]; full += redi[q]; }
-    }
-    __syncthreads();
-    red[tid] = z;
-    __syncthreads();
-    if (tid == 0) {
-        for (int q = 1; q < kThreads; ++q) z += red[q];
+        for (int q = 1; q < W; ++q) { seq += red[q]; z += redz[q]; full += redi[q]; }
         const int T = __ldcg(tokens + nseq);
         double batch = 0.0;
         for (int b = 0; b < ncb; ++b) batch += __ldcg(w.part + (int64_t)nseq * ncb + b);
@@ -514,22 +508,22 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             s[u] = eg[u] = 0.f;
+            if (top[u] == -INFINITY) top[u] = 0.f;  // a row without scores
 #pragma unroll
             for (int q = 0; q < 4 * V; ++q) {
-                // a row without scores: e = 0, but NaN stays
-                e[u][q] = top[u] == -INFINITY ? (h[u][q] == -INFINITY ? 0.f : h[u][q]) : expf(h[u][q] - top[u]);
+                e[u][q] = __expf(h[u][q] - top[u]);
                 s[u] += e[u][q];
                 eg[u] = fmaf(e[u][q], g[u][q], eg[u]);
             }
             if (ptop[u] == -INFINITY) ptop[u] = 0.f;  // no pick has a score: every weight is 0
-            w0[u] = chosen ? expf(x0[u] - ptop[u]) : 0.f;
+            w0[u] = chosen ? __expf(x0[u] - ptop[u]) : 0.f;
             sq[u] = w0[u];
             dq[u] = w0[u] * dg[u];
             if (chosen)
                 for (int t = sub + L; t < k; t += L) {
                     const int p = live[u] ? idx[(r0 + i + u) * k + t] : -1;
                     if (p >= 0 && p < n) {
-                        const float x = expf(mine[u * 2 * CW + p] - ptop[u]);
+                        const float x = __expf(mine[u * 2 * CW + p] - ptop[u]);
                         sq[u] += x;
                         dq[u] = fmaf(x, dgate[(r0 + i + u) * k + t], dq[u]);
                     }
@@ -548,8 +542,8 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
             }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float inv = top[u] == -INFINITY ? 1.f : 1.f / s[u];
-            const float lse = top[u] == -INFINITY ? s[u] : top[u] + logf(s[u]);
+            const float inv = s[u] == 0.f ? 0.f : 1.f / s[u];
+            const float lse = s[u] == 0.f ? 0.f : top[u] + logf(s[u]);
             if (soft) {
                 const float c = eg[u] * inv - cz * lse;
 #pragma unroll
@@ -568,7 +562,7 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
                 for (int t = sub + L; t < k; t += L) {
                     const int p = live[u] ? idx[(r0 + i + u) * k + t] : -1;
                     if (p >= 0 && p < n)
-                        atomicAdd(&add[p], expf(mine[u * 2 * CW + p] - ptop[u]) * iq * (dgate[(r0 + i + u) * k + t] - dot));
+                        atomicAdd(&add[p], __expf(mine[u * 2 * CW + p] - ptop[u]) * iq * (dgate[(r0 + i + u) * k + t] - dot));
                 }
             }
         }
@@ -636,7 +630,7 @@ cudaError_t launch_router_loss(const float* logits, const int32_t* idx, int64_t 
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(router_loss_fold_kernel, dim3((unsigned)nseq + 1, (unsigned)((n + rloss::kFoldCols - 1) / rloss::kFoldCols)),
-                      dim3(rloss::kThreads), 0, stream, m, n, k, off, nseq, (double)alpha, (double)alpha_seq,
+                      dim3(rloss::kFoldThreads), 0, stream, m, n, k, off, nseq, (double)alpha, (double)alpha_seq,
                       (double)z_coef, loss, counts, tokens, f, P, w);
 }
 
