@@ -34,13 +34,6 @@ namespace asp {
 constexpr int kThreads = 256, kGrid = 2 * kNumSMs, kRows = adp::kPad;
 }
 
-__device__ __forceinline__ void split3(float v, __nv_bfloat16 (&p)[3]) {
-    p[0] = __float2bfloat16_rn(v);
-    const float r1 = v - __bfloat162float(p[0]);
-    p[1] = __float2bfloat16_rn(r1);
-    p[2] = __float2bfloat16_rn(r1 - __bfloat162float(p[1]));
-}
-
 // CTA c takes the row blocks (kRows grouped positions) c nb / ctas .. (c + 1) nb / ctas - 1. A group's
 // part of dB in CTA c goes to slot c + g: unique, since each next slot advances the CTA or the group.
 // LPR lanes load a row of dh, NQ 16-byte pieces each. Thread (te, tj) owns dB[NE te + a][NJ tj + b]; du has four

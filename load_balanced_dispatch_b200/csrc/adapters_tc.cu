@@ -10,7 +10,7 @@
 //     warp 1      tcgen05.mma, M = 128 twice (the two halves of the tile share the B operand)
 //     warps 4-11  drain: a thread owns a row; every kDrain K blocks the accumulators are added into fp32
 //                 registers with round-to-nearest adds (the tensor core's own adds truncate, so a long run
-//                 in TMEM would drift); then the epilogue adds s B_a u and stores logits and u.
+//                 in TMEM would drift); then the epilogue has s B_a u formed and stores logits and u.
 // The K blocks of all tiles form one line that is cut into equal runs, one per CTA, whatever the groups'
 // sizes are. A tile that a cut divides is finished by the last of its CTAs to arrive: each writes its
 // partial sums and takes a ticket, nobody waits, and the sums are added in CTA order (the same bits
@@ -35,7 +35,7 @@ __device__ __forceinline__ int64_t line_ctas(int64_t units, int nkb) {
 }
 
 struct AtcShared {
-    uint64_t full[4], empty[4], tfull, tempty;
+    uint64_t full[4], empty[4], tfull, tempty, bfull;
     uint32_t tmem_base;
     int abort_flag;
     int last;
@@ -54,10 +54,22 @@ struct AtcTile {
     static constexpr int B_BYTES = (3 * NP + RP) * 128;
     static constexpr int STAGE = atc::A_BYTES + B_BYTES;
     static constexpr int STAGES = STAGE <= 65536 ? 3 : 2;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + (size_t)NP * RP * 4 + 8 * 32 * 17 * 4 + sizeof(AtcShared);
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + (size_t)NP * 128 + 8 * 32 * 17 * 4 + sizeof(AtcShared);
+    // three bf16 parts of s u, two values a column: over accumulators that have been read, or behind both halves'
+    static constexpr int UCOL = FUSED ? NP : 2 * ACOLS, USTEP = FUSED ? ACOLS : 3 * RP / 2;
+    static constexpr uint32_t TCOLS = FUSED && 2 * ACOLS <= 256 ? 256 : 512;
+    static_assert(FUSED ? NP + 3 * RP / 2 <= ACOLS : 2 * ACOLS + 2 * USTEP <= 512, "the parts of u fit");
     static_assert(2 * ACOLS <= 512, "both halves' accumulators fit the TMEM");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
+
+// v = p[0] + p[1] + p[2], each bf16
+__device__ __forceinline__ void split3(float v, __nv_bfloat16 (&p)[3]) {
+    p[0] = __float2bfloat16_rn(v);
+    const float r1 = v - __bfloat162float(p[0]);
+    p[1] = __float2bfloat16_rn(r1);
+    p[2] = __float2bfloat16_rn(r1 - __bfloat162float(p[1]));
+}
 
 // tile::gather4: four rows of 64 columns (the map's box is one row high)
 __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int r0, int r1,
@@ -79,11 +91,11 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
     using namespace atc;
     using T = AtcTile<NP, RP>;
     constexpr int STAGES = T::STAGES, ACOLS = T::ACOLS;
-    constexpr uint32_t TCOLS = 2 * ACOLS <= 256 ? 256 : 512;
+    constexpr uint32_t TCOLS = T::TCOLS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* sB = reinterpret_cast<float*>(smem + STAGES * T::STAGE);  // [NP][RP] of B_a
-    float* stgs = sB + NP * RP;                                     // 8 warps x [32][17]
+    uint8_t* sB = smem + STAGES * T::STAGE;                         // B_a: [NP] rows of 128 bytes, swizzled
+    float* stgs = reinterpret_cast<float*>(sB + NP * 128);          // 8 warps x [32][17]
     AtcShared* sh = reinterpret_cast<AtcShared*>(stgs + 8 * 32 * 17);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nkb = (d + BK - 1) / BK;
@@ -92,6 +104,7 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
         for (int s = 0; s < STAGES; ++s) { ptx::mbar_init(&sh->full[s], 3); ptx::mbar_init(&sh->empty[s], 1); }
         ptx::mbar_init(&sh->tfull, 1);
         ptx::mbar_init(&sh->tempty, 256);
+        ptx::mbar_init(&sh->bfull, 1);
         sh->abort_flag = 0;
         ptx::fence_barrier_init();
         ptx::prefetch_tensormap(&map_x);
@@ -165,13 +178,14 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                     __syncwarp();
                     if (warp == 0) {
                         // B rows: fused [W0 W1 W2 A], else [W0 A W1 W2]
-#pragma unroll
-                        for (int p = 0; p < 3; ++p)
-                            ptx::tma_load_3d_if(leader, sb + (p * NP + (!T::FUSED && p > 0 ? RP : 0)) * 128, &map_w, bar, kb * BK, ct * NP, p);
-                        if (ad) ptx::tma_load_3d_if(leader, sb + (T::FUSED ? 3 * NP : NP) * 128, &map_a, bar, kb * BK, 0, g);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            if (boxes >> q & 1u) ptx::tma_load_2d_if(leader, st + q * 4096, &map_x, bar, kb * BK, __shfl_sync(0xffffffffu, first, q));
+if (lane >= 8 && lane < 11) {
+                            const int p = lane - 8;
+                            const int row = p * NP + (!T::FUSED && p > 0 ? RP : 0);
+                            ptx::tma_load_3d(sb + row * 128, &map_w, bar, kb * BK, ct * NP, p);
+                        }
+                        if (lane == 11 && ad)
+                            ptx::tma_load_3d(sb + (T::FUSED ? 3 * NP : NP) * 128, &map_a, bar, kb * BK, 0, g);
+                        if (lane < 8 && run) ptx::tma_load_2d(st + lane * 4096, &map_x, bar, kb * BK, first);
                     } else if (gather) {
                         tma_gather4(st + quad * 128, &map_g, bar, kb * BK, rid[0], rid[1], rid[2], rid[3]);
                     }
@@ -233,7 +247,7 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
         const int et = tid - 128;                       // 0 .. 255
         float* stg = stgs + (warp - 4) * 32 * 17;
         const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * ACOLS);
-        uint32_t tphase = 0;
+        uint32_t tphase = 0, bphase = 0;
         bool ok = true;
         for (int64_t pos = lo; pos < hi;) {
             const int64_t unit = pos / nkb;
@@ -280,7 +294,7 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                     }
                 }
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(&sh->tempty);
+                if (kb + kDrain < kb1) ptx::mbar_arrive(&sh->tempty);  // the last arrival comes below
             }
             bool finish = true;
             if (kb0 != 0 || kb1 != nkb) {
@@ -331,17 +345,75 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                     }
                 }
             }
-            if (finish) {  // the same for all eight warps
-                if (ad) {
-                    ptx::named_barrier(1, 256);  // the tile before is done with sB
-                    for (int i = et; i < NP * RP; i += 256) {
-                        const int e = ct * NP + i / RP, q = i % RP;
-                        sB[i] = (e < n && q < r) ? __bfloat162float(bmat[((int64_t)g * n + e) * r + q]) : 0.f;
+            if (finish && ad) {  // the same for all eight warps
+                // s B_a u by the tensor core: s u in three bf16 parts that add up to it, in tensor memory, and B_a
+                // (exact) in shared memory; a few hundred instructions, against 30 to 80 KB of unrolled products
+                if (ok) {
+                    const float s = scale[g];
+                    const uint32_t ut = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(T::UCOL + half * T::USTEP);
+#pragma unroll
+                    for (int q = 0; q < RP; q += 32) {
+                        uint32_t v[3][16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            __nv_bfloat16 a0[3], a1[3];
+                            split3(s * u[q + j], a0);
+                            split3(s * u[q + j + 1], a1);
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) {
+                                const __nv_bfloat162 two(a0[p], a1[p]);
+                                v[p][j / 2] = *reinterpret_cast<const uint32_t*>(&two);
+                            }
+                        }
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) ptx::tmem_st16_issue(ut + (uint32_t)(p * (RP / 2) + q / 2), v[p]);
                     }
-                    ptx::named_barrier(1, 256);
+                    ptx::tmem_wait_st();
                 }
-                // 16 columns at a time through the warp's staging rows: rolled loops over the columns (unrolled in
-                // full, the NP x RP products are 30 to 80 KB of code that every launch fetches anew) and stores of 64-byte pieces
+                for (int i = et; i < NP * RP / 8; i += 256) {  // 16-byte piece i % (RP / 8) of row i / (RP / 8)
+                    const int e = i / (RP / 8), c8 = i % (RP / 8), col = ct * NP + e;
+                    const __nv_bfloat16* src = bmat + ((int64_t)g * n + col) * r + 8 * c8;
+                    uint32_t v[4] = {0u, 0u, 0u, 0u};
+                    if (col < n) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (8 * c8 + j < r) v[j / 2] |= (uint32_t)__bfloat16_as_ushort(src[j]) << (16 * (j & 1));
+                    }
+                    *reinterpret_cast<uint4*>(sB + e * 128 + ((c8 ^ (e & 7)) * 16)) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+                ptx::fence_proxy_async_shared();
+                ptx::tc_fence_before();
+                ptx::named_barrier(1, 256);
+                if (et == 0) {
+                    ptx::tc_fence_after();
+                    const uint32_t idesc = ptx::idesc_bf16_f32(128, NP);
+                    const uint64_t bdesc = ptx::sw128_kmajor_desc(ptx::smem_u32(sB));
+                    for (int h = 0; h < (cnt > 128 ? 2 : 1); ++h)
+                        for (int p = 2; p >= 0; --p)  // the small parts first
+                            for (int k = 0; 16 * k < r; ++k)
+                                ptx::umma_bf16_ts(tmem + (uint32_t)(h * ACOLS), tmem + (uint32_t)(T::UCOL + h * T::USTEP + p * (RP / 2) + 8 * k),
+                                                  bdesc + 2 * k, idesc, (p != 2 || k != 0) ? 1u : 0u);
+                    ptx::umma_commit(&sh->bfull);
+                }
+                __syncwarp();
+                if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->bfull, bphase, abort_flag));
+                bphase ^= 1u;
+                ptx::tc_fence_after();
+                if (ok && mine) {
+#pragma unroll
+                    for (int q = 0; q < NP / 16; ++q) {
+                        uint32_t v[16];
+                        ptx::tmem_ld16_issue(trow + (uint32_t)(q * 16), v);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[q * 16 + j] = __fadd_rn(acc[q * 16 + j], __uint_as_float(v[j]));
+                    }
+                }
+                ptx::tc_fence_before();
+            }
+            if (ok) ptx::mbar_arrive(&sh->tempty);  // the accumulators are free for the next unit
+            if (finish) {
+                // 16 columns at a time through the warp's staging rows: stores of 64-byte pieces
                 if (ok && half * 128 + quad * 32 < cnt) {  // the same for the warp
                     const int32_t out = row < cnt ? plan.perm[p0 + row] : -1;
                     float* mine = stg + lane * 17;
@@ -365,35 +437,11 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                             }
                         }
                     }
-                    if (ad) {
-                        const float s = scale[g];
-#pragma unroll
-                        for (int j = 0; j < RP; ++j) u[j] *= s;
-                    }
 #pragma unroll
                     for (int e0 = 0; e0 < NP; e0 += 16) {
                         if (ct * NP + e0 < n) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) mine[j] = acc[e0 + j];
-                            if (ad) {
-#pragma unroll 4
-                                for (int j = 0; j < 16; ++j) {
-                                    float t0 = 0.f, t1 = 0.f;
-#pragma unroll
-                                    for (int q8 = 0; q8 < RP; q8 += 16) {
-                                        if (q8 >= r) continue;
-#pragma unroll
-                                        for (int q = q8; q < q8 + 16; q += 4) {
-                                            const float4 b4 = *reinterpret_cast<const float4*>(sB + (e0 + j) * RP + q);
-                                            t0 = fmaf(u[q], b4.x, t0);
-                                            t1 = fmaf(u[q + 1], b4.y, t1);
-                                            t0 = fmaf(u[q + 2], b4.z, t0);
-                                            t1 = fmaf(u[q + 3], b4.w, t1);
-                                        }
-                                    }
-                                    mine[j] += t0 + t1;
-                                }
-                            }
                             store16(logits, n, ct * NP + e0);
                         }
                     }
