@@ -417,14 +417,19 @@ if (lane >= 8 && lane < 11) {
                 if (ok && half * 128 + quad * 32 < cnt) {  // the same for the warp
                     const int32_t out = row < cnt ? plan.perm[p0 + row] : -1;
                     float* mine = stg + lane * 17;
+                    int32_t to[16];  // the row of each of this lane's pieces
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) to[i] = __shfl_sync(0xffffffffu, out, 2 * i + (lane >> 4));
+                    const float* from = stg + (lane >> 4) * 17 + (lane & 15);
                     auto store16 = [&](float* dst, int width, int col) {
+                        const int cc = col + (lane & 15);
                         __syncwarp();
-#pragma unroll 4
-                        for (int i = 0; i < 16; ++i) {
-                            const int q = 2 * i + (lane >> 4), cc = col + (lane & 15);
-                            const int32_t to = __shfl_sync(0xffffffffu, out, q);
-                            if (to >= 0 && cc < width) dst[(int64_t)to * width + cc] = stg[q * 17 + (lane & 15)];
-                        }
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = from[i * 34];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (to[i] >= 0 && cc < width) dst[(int64_t)to[i] * width + cc] = v[i];
                         __syncwarp();
                     };
                     if (hidden && ct == 0) {
@@ -459,10 +464,11 @@ if (lane >= 8 && lane < 11) {
 }
 
 // ---- host side
-// Column tile of the logits: all n in one tile where the accumulators fit, else equal tiles.
-static void atc_tile(int n, int r, int& np, int& rp, int& nct) {
+// Column tile of the logits: all n in one tile where the accumulators fit, else equal tiles; 64 columns at most where
+// that gives more CTAs work (8191 rows of 768 columns, n 128: MEASURE).
+static void atc_tile(int64_t m, int n, int r, int& np, int& rp, int& nct) {
     rp = r <= 32 ? 32 : 64;
-    const int most = rp == 32 ? 128 : 64;
+    const int most = rp == 32 && 2 * (m / atc::BM + 1) > kNumSMs ? 128 : 64;
     nct = (n + most - 1) / most;
     np = ((n + nct - 1) / nct + 31) / 32 * 32;
 }
@@ -478,7 +484,7 @@ static int64_t atc_tiles(int64_t m, int na) { return m / atc::BM + na + 1; }
 
 static size_t atc_layout(int64_t m, int d, int n, int r, int na, AtcWs* w, char* base) {
     int np, rp, nct;
-    atc_tile(n, r, np, rp, nct);
+    atc_tile(m, n, r, np, rp, nct);
     size_t off = 0;
     auto take = [&](size_t bytes) { char* p = base + off; off += (bytes + 255) & ~size_t(255); return p; };
     off = adapter_plan_layout(m, na, w ? &w->plan : nullptr, base);
@@ -505,7 +511,7 @@ static cudaError_t launch_router_adapters_tc(const __nv_bfloat16* x, const float
                                              int d, int n, int r, int na, float* logits, float* hidden, void* workspace,
                                              cudaStream_t stream) {
     int np, rp, nct;
-    atc_tile(n, r, np, rp, nct);
+    atc_tile(m, n, r, np, rp, nct);
     AtcWs w;
     atc_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
     PrepExtra extra = {};
