@@ -506,7 +506,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
 
 // ---------------------------------------------------------------- contraction over rows
 namespace rct {
-constexpr int kThreads = 384, kDrain = 4, BD = 256, BK = adp::kPad;
+constexpr int kThreads = 384, kDrain = 4, kRun = 8, BD = 256, BK = adp::kPad;
 }
 
 struct RctShared {
@@ -565,7 +565,18 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
     volatile int* abort_flag = &sh->abort_flag;
     const int ndt = (d + BD - 1) / BD, nct = (ncols + C - 1) / C, U = ndt * nct;
     const int64_t total = (int64_t)(plan.goff[one ? na + 1 : na] / BK) * U;
-    int64_t ctas = total / kLeastRun;  // the units' lengths differ: cut wherever it falls
+    // CTAs: runs of a unit's length on average, but not of more than kRun K blocks, while SMs are left (runs of 16 blocks
+    // whatever the units were took 46 us for 100 rows of 40 adapters, d 2328: a CTA then had 16 units of one block each)
+    int64_t units = U;
+    if (!one) {
+        int used = 0;
+        for (int g0 = 0; g0 < na; g0 += kThreads)
+            used += __syncthreads_count(g0 + tid < na && plan.goff[min(g0 + tid, na - 1) + 1] > plan.goff[min(g0 + tid, na - 1)]);
+        units *= used;
+    }
+    int64_t run = units > 0 ? total / units : 1;
+    run = run < 1 ? 1 : (run > kRun ? kRun : run);
+    int64_t ctas = total / run;
     ctas = ctas < 1 ? 1 : (ctas > gridDim.x ? gridDim.x : ctas);
     const int64_t c = blockIdx.x;
     const int64_t lo = c < ctas ? c * total / ctas : total, hi = c < ctas ? (c + 1) * total / ctas : total;
