@@ -12,8 +12,10 @@ from dataclasses import dataclass
 import torch
 
 from . import (MOE_QB_MIDPOINT, MOE_QB_STEP, MOE_SIGMOID, MOE_SOFTMAX, moe_balance_assign, moe_balance_stats,
-               moe_capacity_slots, moe_combine, moe_dispatch_tokens, moe_expert_ffn, moe_expert_ffn_combine,
-               moe_expert_ffn_gather, moe_router_prepare, moe_router_topk, lib)
+               moe_capacity_slots, moe_combine, moe_combine_grad, moe_dispatch_tokens, moe_expert_ffn,
+               moe_expert_ffn_combine, moe_expert_ffn_gather, moe_router_adapters, moe_router_adapters_grad,
+               moe_router_adapters_grad_workspace_size, moe_router_adapters_workspace_size, moe_router_loss,
+               moe_router_loss_grad, moe_router_loss_workspace_size, moe_router_prepare, moe_router_topk, lib)
 
 
 @dataclass
@@ -90,6 +92,7 @@ class MoELayer:
         # data-parallel replicas: set by enable_global_stats(); the Loss-Free bias then follows the
         # pooled counts of every rank instead of this rank's
         self.global_stats = None
+        self.adapters = None  # set by enable_adapters(): low-rank adapters beside the router projection
 
     STAGES = ("router", "capacity", "dispatch", "ffn", "combine", "stats")
 
@@ -97,6 +100,14 @@ class MoELayer:
         s, b, w = self.shape, self.buf, self.w
         if i == 0:
             fn = MOE_SOFTMAX if s.score_fn == "softmax" else MOE_SIGMOID
+            ad = self.adapters
+            if ad is not None:
+                moe_router_adapters(x, w["w_r"], ad["a"], ad["b"], ad["adapter_idx"], ad["scale"], logits=b["logits"],
+                                    hidden=b["hidden"], workspace=self.ws["adapters"], stream=st)
+                moe_router_topk(None, None, s.n, s.k, fn, s.renorm_topk, rank_bias=w.get("rank_bias"),
+                                logits_in=b["logits"], probs_out=b["probs"], topk_idx=b["topk_idx"],
+                                topk_gate=b["topk_gate"], stream=st)
+                return
             moe_router_topk(x, None if self.router_prepared else w["w_r"], s.n, s.k, fn, s.renorm_topk,
                             rank_bias=w.get("rank_bias"),
                             probs_out=b["probs"], topk_idx=b["topk_idx"], topk_gate=b["topk_gate"],
@@ -192,6 +203,50 @@ class MoELayer:
         events[len(self.graphs)].record(st)
         return self.buf["y"]
 
+    def enable_adapters(self, a, b, scale, adapter_idx) -> None:
+        """Give the router a low-rank adapter per token: from now on logits_i = x_i W_r + scale_q B_q (A_q x_i) with
+        q = adapter_idx[i] (-1: none), for a [na, r, d] and b [na, n, r] of the layer's dtype, scale [na] fp32 and
+        adapter_idx [m] int32. The tensors are used in place: a captured forward follows their contents. The layer then
+        keeps what `router_backward` reads, among it the expert rows (ybuf), so one pick per token runs FFN and combine
+        apart."""
+        s, dev = self.shape, self.device
+        na, r = a.shape[:2]
+        self.adapters = dict(a=a, b=b, scale=scale, adapter_idx=adapter_idx)
+        f32, u8 = torch.float32, torch.uint8
+        self.buf["logits"] = torch.empty((s.m, s.n), dtype=f32, device=dev)
+        self.buf["hidden"] = torch.empty((s.m, r), dtype=f32, device=dev)
+        if self.ffn_combine:
+            self.ffn_combine = False
+            self.buf["ybuf"] = torch.empty((self.rows_max, s.d), dtype=s.dtype, device=dev)
+        size = moe_router_adapters_workspace_size(s.m, s.d, s.n, r, na, s.dtype)
+        self.ws["adapters"] = torch.empty((max(size, 1),), dtype=u8, device=dev)
+
+    def router_backward(self, x, dy, seq_offsets, token_mask=None, alpha_seq=0.0, z_coef=0.0, dloss=None,
+                        want_dx=True, want_dw_r=False, stream=None) -> dict:
+        """The backward of the router after a forward with adapters (enable_adapters): from dy = dL/dy and the
+        router's own losses over the ragged sequences (`moe_router_loss` with this layer's alpha) to the gradients of
+        the adapters. Returns dict(da, db, dw_r or None, dx or None (through the router alone), dybuf (of the expert
+        rows, for the experts' backward), dgate, dlogits and moe_router_loss's loss, counts, tokens, f, P)."""
+        if self.adapters is None:
+            raise RuntimeError("router_backward needs enable_adapters() and a forward")
+        s, b, w, ad = self.shape, self.buf, self.w, self.adapters
+        fn = MOE_SOFTMAX if s.score_fn == "softmax" else MOE_SIGMOID
+        coef = dict(token_mask=token_mask, score_fn=fn, alpha=s.alpha, alpha_seq=alpha_seq, z_coef=z_coef, stream=stream)
+        na, r = ad["a"].shape[:2]
+        nseq = seq_offsets.shape[0] - 1
+        for key, size in (("loss", moe_router_loss_workspace_size(s.m, s.n, nseq)),
+                          ("adapters_grad", moe_router_adapters_grad_workspace_size(s.m, s.d, s.n, r, na, s.dtype))):
+            if key not in self.ws or self.ws[key].numel() < size:
+                self.ws[key] = torch.empty((size,), dtype=torch.uint8, device=self.device)
+        dybuf, dgate = moe_combine_grad(dy, b["ybuf"], b["dest_row"], b["topk_gate"], stream=stream)
+        out = moe_router_loss(b["logits"], b["topk_idx"], seq_offsets, workspace=self.ws["loss"], **coef)
+        dlogits = moe_router_loss_grad(b["logits"], b["topk_idx"], seq_offsets, out["counts"], out["tokens"], dloss=dloss,
+                                       dgate=dgate, renorm_topk=s.renorm_topk, **coef)
+        dx, da, db, dw_r = moe_router_adapters_grad(
+            dlogits, x, w["w_r"], ad["a"], ad["b"], ad["adapter_idx"], ad["scale"], b["hidden"], want_dx=want_dx,
+            want_dw_r=want_dw_r, workspace=self.ws["adapters_grad"], stream=stream)
+        return dict(out, da=da, db=db, dw_r=dw_r, dx=dx, dybuf=dybuf, dgate=dgate, dlogits=dlogits)
+
     def enable_global_stats(self, m_total: int, group=None) -> None:
         """Pool the statistics over data-parallel ranks: after each forward, `sync_global_stats`
         sums this rank's totals with every other rank's (one all-reduce of 2 n doubles) and
@@ -233,6 +288,9 @@ class MoELayer:
         sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
         rows_mode = s.n <= 64 and (s.m + 127) // 128 > sms
         router = 2 if (bf16 and s.n <= 128 and not rows_mode) else 1
+        if self.adapters is not None:  # grouping + tensor-core projection (one launch for few rows or fp32), then top-k
+            na, r = self.adapters["a"].shape[:2]
+            router = (2 if moe_router_adapters_workspace_size(s.m, s.d, s.n, r, na, s.dtype) else 1) + 1
         capacity = 2
         dispatch = 1 if self.uses_dispatch() else 0
         if self.ffn_combine:  # the FFN with the combine in its epilogue, plus the dropped rows
