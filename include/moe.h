@@ -517,7 +517,8 @@ MOE_API moe_status moe_balance_global(const double* totals, int64_t m_total, int
  *  logits      [m, n] fp32 out. hidden [m, r] fp32 out (for the backward), or NULL.
  *  Limits: m <= 2^24; 1 <= r <= 64; 1 <= n_adapters <= 1024; d a multiple of 8 (bf16) or
  *  4 (fp32), at most 2^20. Arrays 16-byte aligned. All sums fp32-accurate: with bf16 x, W_r
- *  enters the tensor cores as three bf16 parts whose sum is its fp32 value.
+ *  enters the tensor cores as three bf16 parts whose sum is its fp32 value. A NaN or infinity
+ *  in x makes its own row's results NaN or infinite and no other row's.
  *  Workspace: moe_router_adapters_workspace_size bytes, any contents; one per call in flight.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE.
  */
@@ -539,7 +540,8 @@ MOE_API moe_status moe_router_adapters(const void* x, moe_dtype x_dtype, const f
  *  da, db  [n_adapters, r, d] and [n_adapters, n, r] fp32 out (overwritten; zero for an
  *          adapter without rows). dw_r [d, n] fp32 out, or NULL (shared projection frozen).
  *  The other arguments, limits and alignment are moe_router_adapters'. Sums run in a fixed
- *  order without atomics: the same call gives the same bits.
+ *  order: the same call gives the same bits. A NaN or infinity in a row of dlogits or x reaches
+ *  that row of dx, its adapter's da and db, and dw_r.
  */
 MOE_API size_t moe_router_adapters_grad_workspace_size(int64_t m, int32_t d, int32_t n, int32_t r,
                                                        int32_t n_adapters, moe_dtype x_dtype);
@@ -566,7 +568,7 @@ MOE_API moe_status moe_router_adapters_grad(const float* dlogits, const void* x,
  *              last sequence are padding. Offsets that descend or leave [0, m] set the device
  *              error word (results are then unspecified).
  *  token_mask  [m] uint8, 0: the token counts for nothing; NULL: every token counts.
- *              Padding and masked rows' logits and picks are not read.
+ *              What padding and masked rows hold (NaN, picks out of range) does not matter.
  *  For the T counted tokens of a sequence, or of all of them (row nseq of the tables):
  *   f_i = count_i / (k T), P_i = mean p_i (both 0 when T = 0).
  *  loss   [4] out: total, alpha n sum_i f_i P_i over the whole batch, alpha_seq times the mean

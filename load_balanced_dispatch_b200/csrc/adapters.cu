@@ -253,11 +253,10 @@ static cudaError_t launch_adapter_prep(const int32_t* idx, int64_t m, int na, co
 // batches of few rows (adapters_run.cu has the rule). In a CTA, eight warps read its slice of W_r once for the four
 // rows (a thread: four columns, every KL-th row of the slice) and eight form u (a warp: four products at a time, lanes
 // along d; A_a is read once for the rows when they share it). These are other warps (512 threads) while all clusters
-// surely run at once (and W_r is not the larger part), and the same ones (256 threads, three CTAs per SM) for more rows: 8 against 11 us for 32 rows of 2048
-// columns, but 102 against 54 us for 4096 rows of 512. The slices' sums meet in distributed
-// shared memory, where each CTA finishes a part of the columns. Nothing is grouped and one launch does all, so a step
-// of few rows is bound by the latency of that chain;
-// a large batch by the reads of A_a from L2, 1.5 us per 2^20 of m d r.
+// surely run at once and W_r is not the larger part, and the same ones (256 threads, three CTAs per SM) for more rows:
+// 8 against 11 us for 32 rows of 2048 columns, but 102 against 54 us for 4096 rows of 512. The slices' sums meet in
+// distributed shared memory, where each CTA finishes a part of the columns. Nothing is grouped and one launch does
+// all, so a step of few rows is bound by the latency of that chain, a large batch by the reads of A_a and W_r from L2.
 constexpr int kFewRows = 4, kFewSlice = 512;  // rows of a cluster; columns of d in shared memory at a time
 
 // Sums of four values over the warp, in six shuffles: lane l gets the sum of t[l / 8].

@@ -3,15 +3,17 @@
 
 namespace moe {
 
-// Which forward: adapters_few_kernel for fp32, and for bf16 while its reads of A_a (m d r) stay small. Measured, few
-// rows against tensor cores: 20 against 25 us for 1024 rows (d 512, n 64, r 16), 30 against 29 for 2048; 32 against 33
-// for 512 rows (d 2048), 60 against 37 for 1024; 66 against 68 for 256 rows (d 4096, n 256), 98 against 72 for 512.
-static bool adapters_few(int64_t m, int d, int r, moe_dtype dt) {
-    return dt == MOE_F32 || (m <= 2048 && m * d * r <= (int64_t)1 << 24);
+// Which forward: adapters_few_kernel for fp32, and for bf16 while its reads of A_a and W_r from L2 (which grow with
+// m d (8 r + n)) cost less than the grouped tensor-core pass takes at least. Measured, few rows against tensor cores:
+// 12 against 16 us for 512 rows (d 512, n 64, r 16), 29 against 20 for 2048; 13 against 24 for 128 rows of d 2048, 31
+// against 25 for 512; 20 against 23 for 64 rows (d 1024, n 128, r 64), 27 against 23 for 128; 10 against 13 for 2048
+// rows of d 64, 16 against 13 for 4096.
+static bool adapters_few(int64_t m, int d, int n, int r, moe_dtype dt) {
+    return dt == MOE_F32 || (m <= 2048 && m * d * (8 * r + n) <= (int64_t)1 << 26);
 }
 
 size_t router_adapters_workspace_bytes(int64_t m, int32_t d, int32_t n, int32_t r, int32_t na, moe_dtype dt) {
-    if (m < 1 || d < 1 || n < 1 || n > kMaxExperts || r < 1 || r > kMaxRank || na < 1 || adapters_few(m, d, r, dt)) return 0;
+    if (m < 1 || d < 1 || n < 1 || n > kMaxExperts || r < 1 || r > kMaxRank || na < 1 || adapters_few(m, d, n, r, dt)) return 0;
     return atc_layout(m, d, n, r, na, nullptr, nullptr);
 }
 
@@ -30,7 +32,7 @@ cudaError_t launch_router_adapters(const void* x, moe_dtype dt, const float* w_r
                                    static_cast<const float*>(b), idx, scale, m, d, n, r, na, logits, hidden, stream);
     const __nv_bfloat16 *xb = static_cast<const __nv_bfloat16*>(x), *ab = static_cast<const __nv_bfloat16*>(a),
                         *bb = static_cast<const __nv_bfloat16*>(b);
-    if (adapters_few(m, d, r, dt))
+    if (adapters_few(m, d, n, r, dt))
         return launch_adapters_few(xb, w_r, ab, bb, idx, scale, m, d, n, r, na, logits, hidden, stream);
     return launch_router_adapters_tc(xb, w_r, ab, bb, idx, scale, m, d, n, r, na, logits, hidden, workspace, stream);
 }
