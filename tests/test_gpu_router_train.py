@@ -83,6 +83,7 @@ SHAPES = [  # m, d, n, r, na, dtype, order
     (256, 128, 64, 16, 4, "bf16", "none"), (2000, 128, 96, 32, 1, "bf16", "mixed"), (37, 8, 1, 1, 2, "bf16", "mixed"),
     (3000, 64, 16, 8, 1024, "bf16", "mixed"), (20000, 64, 128, 8, 4, "bf16", "runs"),
     (19500, 72, 90, 32, 3, "bf16", "mixed"), (2600, 512, 64, 16, 6, "bf16", "runs"), (2100, 200, 128, 32, 5, "bf16", "mixed"),
+    (2500, 128, 256, 16, 5, "bf16", "runs"), (20000, 64, 200, 16, 3, "bf16", "runs"), (20500, 40, 256, 33, 2, "bf16", "mixed"),
     (2200, 264, 40, 64, 9, "bf16", "runs"), (2300, 128, 20, 40, 2, "bf16", "one"),
     (1, 4, 1, 1, 1, "fp32", "mixed"), (1024, 64, 8, 4, 3, "fp32", "runs"), (333, 1000, 64, 16, 5, "fp32", "mixed"),
     (517, 36, 256, 64, 9, "fp32", "runs"), (129, 260, 17, 5, 33, "fp32", "mixed"), (600, 132, 100, 20, 2, "fp32", "one"),
