@@ -496,6 +496,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
             if (++buf == 2) { buf = 0; bphase ^= 1u; }
         }
     }
+    ptx::settle_after_abort(abort_flag);
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -772,6 +773,7 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
             pos += kb1 - kb0;
         }
     }
+    ptx::settle_after_abort(abort_flag);
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 1) {

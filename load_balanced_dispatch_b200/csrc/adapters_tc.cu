@@ -41,12 +41,6 @@ struct AtcShared {
     int last;
 };
 
-// The part of a CTA's run that lies in one unit (row tile x column tile).
-struct AtcSegment {
-    int64_t unit;
-    int kb0, kb1;
-};
-
 template <int NP, int RP>
 struct AtcTile {
     static constexpr bool FUSED = 3 * NP + RP <= 256;
@@ -455,6 +449,7 @@ if (lane >= 8 && lane < 11) {
             pos += kb1 - kb0;
         }
     }
+    ptx::settle_after_abort(abort_flag);
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 1) {

@@ -59,6 +59,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// Before a CTA leaves after a wait that gave up: copies and MMAs that it has in flight end within microseconds, and
+// their shared memory must not pass to another CTA before that (about 100 us; nothing when no wait gave up).
+__device__ __forceinline__ void settle_after_abort(volatile int* abort_flag) {
+    if (!*abort_flag) return;
+    const long long t0 = clock64();
+    while (clock64() - t0 < 200000) __nanosleep(1000);
+}
+
 // Contiguous bulk copy global -> this CTA's shared memory, completing on an mbarrier (no
 // multicast). Both addresses 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
