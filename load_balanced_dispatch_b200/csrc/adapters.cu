@@ -20,6 +20,7 @@ constexpr int kPad = 64;        // a group's rows are padded to this many in the
 constexpr int kTile = 256;      // rows of a tensor-core row tile
 constexpr int kPlanThreads = 1024;
 constexpr int kCluster = 8;     // CTAs that group the rows of a large batch
+constexpr int kPrepRows = 256;  // rows of the adapters that a block scales
 constexpr int kClusterRows = 2048;  // above this many rows (one CTA: 6 us for 8191 rows, 62 us for 65536)
 }  // namespace adp
 
@@ -58,12 +59,36 @@ __device__ __forceinline__ int group_at(const int32_t* __restrict__ start, int g
 // What the blocks behind the plan's do: parts of W_r for the tensor cores, or du for the fp32 kernels.
 struct PrepExtra {
     const float* w_r;       // W_r [d, n] ...
-    int d, n, nk, parts;    // ... as bf16 parts that add up to it: three as [3, n, d] (transposed, for x W_r), or two
-    __nv_bfloat16* wparts;  // as [2, d, nk], nk >= n with zeros behind n (for dh W_r^T)
+    int d, n;
+    __nv_bfloat16* wparts;  // ... for x W_r: three bf16 parts that add up to it, [3, n, d] (transposed)
+    // ... for dh W_r^T: row t times 2^k_t as two fp16 parts [2, d, nk], nk >= n with zeros behind n; 2^-k_t; and the
+    // adapters' columns t times 2^k_t, [na r, d], since their products are added to the same sums
+    __half* wscaled;
+    int nk, arows;
+    __nv_bfloat16* cinv;
+    const __nv_bfloat16* a;
+    __nv_bfloat16* ascaled;
     const float *dh, *b, *scale;  // du_ij = s_a sum_e dh_ie B_a[e, j], a warp per row, lanes along j
     int r;
     float* du;
 };
+
+// k such that values of magnitude up to `top` are below 2^14 after a product with 2^k (top 0, inf or NaN: 0), at most
+// `most`. Two fp16 parts then hold such a value to 2^-22 of itself or 2^-39 of the largest, and a product of two of
+// them, or the sum of 256, is far from the ends of fp32.
+__device__ __forceinline__ int fit_exponent(float top, int most) {
+    if (!(top > 0.f) || isinf(top)) return 0;
+    int e;
+    frexpf(top, &e);  // top < 2^e
+    return min(14 - e, most);
+}
+constexpr int kRowExponent = 100, kColExponent = 60;  // the most for rows of dh and of W_r
+
+// v to within 2^-22 of itself (or 2^-25)
+__device__ __forceinline__ void split2h(float v, __half (&p)[2]) {
+    p[0] = __float2half_rn(v);
+    p[1] = __float2half_rn(v - __half2float(p[0]));
+}
 
 // Stable grouping of the rows by adapter by one cluster (blocks 0 .. its size - 1). Each warp takes a run of
 // consecutive rows: a histogram per warp, sums over the warps and the CTAs before, then each warp places its rows;
@@ -96,27 +121,46 @@ adapter_prep_kernel(const int32_t* __restrict__ idx, int64_t m, int na, AdapterP
             return;
         }
         __shared__ float tile[32][33];
-        const int d = x.d, n = x.n, nb = (n + 31) / 32;
-        const int t0 = b / nb * 32, j0 = b % nb * 32;
-        if (t0 >= d) return;
-        float v = (t0 + wid < d && j0 + lane < n) ? x.w_r[(int64_t)(t0 + wid) * n + j0 + lane] : 0.f;
-        int j = j0 + lane, t = t0 + wid;
-        if (x.parts == 3) {
-            tile[wid][lane] = v;
+        const int d = x.d, n = x.n;
+        if (x.wscaled) {  // rows t0 .. t0 + 31 of W_r, a warp each, and kPrepRows rows of the adapters in these columns
+            const int nt = (d + 31) / 32, t0 = b % nt * 32, q0 = b / nt * kPrepRows, t = t0 + wid;
+            if (q0 > 0 && q0 >= x.arows) return;
+            float top = 0.f;
+            if (t < d)
+                for (int j = lane; j < n; j += 32) top = fmaxf(top, fabsf(x.w_r[(int64_t)t * n + j]));
+            const int k = fit_exponent(warp_max(top), kColExponent);
+            const float c = ldexpf(1.f, k);
+            if (lane == 0) tile[0][wid] = c;
+            if (q0 == 0 && t < d) {
+                if (lane == 0) x.cinv[t] = __float2bfloat16_rn(ldexpf(1.f, -k));
+                for (int j = lane; j < x.nk; j += 32) {
+                    __half p[2];
+                    split2h(j < n ? x.w_r[(int64_t)t * n + j] * c : 0.f, p);
+                    x.wscaled[(int64_t)t * x.nk + j] = p[0];
+                    x.wscaled[((int64_t)d + t) * x.nk + j] = p[1];
+                }
+            }
             __syncthreads();
-            j = j0 + wid;
-            t = t0 + lane;
-            v = tile[lane][wid];
+            if (t0 + lane < d)
+                for (int q = q0 + wid; q < min(q0 + kPrepRows, x.arows); q += 32)
+                    x.ascaled[(int64_t)q * d + t0 + lane] =
+                        __float2bfloat16_rn(__bfloat162float(x.a[(int64_t)q * d + t0 + lane]) * tile[0][lane]);
+            return;
         }
-        if (j >= (x.parts == 3 ? n : x.nk) || t >= d) return;
+        const int nb = (n + 31) / 32, t0 = b / nb * 32, j0 = b % nb * 32;
+        if (t0 >= d) return;
+        tile[wid][lane] = (t0 + wid < d && j0 + lane < n) ? x.w_r[(int64_t)(t0 + wid) * n + j0 + lane] : 0.f;
+        __syncthreads();
+        const int j = j0 + wid, t = t0 + lane;
+        const float v = tile[lane][wid];
+        if (j >= n || t >= d) return;
         const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
         const float r1 = v - __bfloat162float(p0);
         const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
-        const int64_t o = x.parts == 3 ? (int64_t)j * d + t : (int64_t)t * x.nk + j;
-        const int64_t plane = x.parts == 3 ? (int64_t)n * d : (int64_t)d * x.nk;
+        const int64_t o = (int64_t)j * d + t, plane = (int64_t)n * d;
         x.wparts[o] = p0;
         x.wparts[plane + o] = p1;
-        if (x.parts == 3) x.wparts[2 * plane + o] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
+        x.wparts[2 * plane + o] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
         return;
     }
     int* own = hist + 32 * G;
@@ -231,6 +275,7 @@ static cudaError_t launch_adapter_prep(const int32_t* idx, int64_t m, int na, co
     const int cluster = m > adp::kClusterRows ? adp::kCluster : 1;
     int64_t extra = 0;
     if (x.wparts) extra = (int64_t)((x.d + 31) / 32) * ((x.n + 31) / 32);
+    if (x.wscaled) extra = (int64_t)((x.d + 31) / 32) * ((x.arows + adp::kPrepRows - 1) / adp::kPrepRows);
     if (x.du) extra = (m + 31) / 32;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(cluster + (extra + cluster - 1) / cluster * cluster));

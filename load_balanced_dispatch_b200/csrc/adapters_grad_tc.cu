@@ -1,18 +1,22 @@
 // adapters_grad_tc.cu -- backward of the router projection with adapters on the tensor cores (bf16
 // activations). The operator is described in adapters.cu; rows are in the grouped order of AdapterPlan.
 //
-//   adapters_split_kernel     per row: du = s B_a^T dh, and dh and du as bf16 parts whose sum is the fp32
-//                             value (three parts for the weight gradients, of which dx uses two); dB on
-//                             the way, each CTA's sums over its run of rows to a slot of its own
+//   adapters_split_kernel     per row: du = s B_a^T dh, and dh and du as 16-bit parts that add up to the fp32
+//                             value (bf16 for the weight gradients, scaled fp16 and bf16 for dx); dB on the way,
+//                             each CTA's sums over its run of rows to a slot of its own
 //   adapters_dx_tc_kernel     dx = dh W_r^T + du A_a: the parts of dh and du of a row tile stay in shared
 //                             memory while the parts of W_r and A_a stream past, columns of d at a time
 //   rows_contract_tc_kernel   dA_a = du^T x and dW_r = x^T dh: a contraction over rows, x read once per 64
 //                             columns of the other operand
 //   adapters_fold_kernel      dB from the slots, zeros for adapters without rows
 //
-// dx is rounded to bf16 at the end, so two parts a side and three of their four products (2^-16 of a
-// product is left out) lose nothing against that rounding; one part a side would add errors of the
-// rounding's own size. The weight gradients are fp32, so x (exact in bf16) meets three parts.
+// All sums are right to fp32. For the weight gradients x (exact in bf16) meets three bf16 parts. For dx both sides
+// are fp32: dh and W_r are multiplied by powers of two (one a row of dh, one a row of W_r), so that two fp16 parts
+// hold 22 bits of each value, and three of their four products are formed (the fourth is below 2^-22); du A_a, du in
+// three bf16 parts, is scaled alike and added to the same sums; the drain takes the powers out again. Two bf16 parts a
+// side without scales have 16 bits, which shows in dx where W_r's rows have much in common (the gradient of a
+// softmax adds up to zero, so that cancels). dx of 65536 rows, d 4096, n 64, rank 16: 131 us with two bf16 parts,
+// 143 us so, 205 us with three bf16 parts and six products.
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -34,6 +38,15 @@ namespace asp {
 constexpr int kThreads = 256, kGrid = 2 * kNumSMs, kRows = adp::kPad;
 }
 
+// What the contractions and dx read, [rows in the grouped order]. Null pointers: not wanted.
+struct SplitOut {
+    __nv_bfloat16 *dhp;  // [3, m_pad, nk] dh in three bf16 parts (dW_r)
+    __nv_bfloat16 *dup;  // [m_pad, 128 or 192] du in three bf16 parts beside one another (dA)
+    __half* dhs;         // [2, m_pad, nk] dh times 2^k of its row in two fp16 parts (dx)
+    __nv_bfloat16 *dus;  // as dup, du times 2^k (dx)
+    float* rinv;         // [m_pad] 2^-k
+};
+
 // CTA c takes the row blocks (kRows grouped positions) c nb / ctas .. (c + 1) nb / ctas - 1. A group's
 // part of dB in CTA c goes to slot c + g: unique, since each next slot advances the CTA or the group.
 // LPR lanes load a row of dh, NQ 16-byte pieces each. Thread (te, tj) owns dB[NE te + a][NJ tj + b]; du has four
@@ -42,8 +55,7 @@ template <int NE, int NJ, int RP>
 __global__ void __launch_bounds__(asp::kThreads)
 adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hidden,
                       const __nv_bfloat16* __restrict__ bmat, const float* __restrict__ scale, int n, int r, int na,
-                      AdapterPlan plan, int nk, int planes, int64_t mp, __nv_bfloat16* __restrict__ dhp,
-                      __nv_bfloat16* __restrict__ dup, float* __restrict__ slots) {
+                      AdapterPlan plan, int nk, int64_t mp, SplitOut out, float* __restrict__ slots) {
     using namespace asp;
     constexpr int NP = NE * 32, HS = NP + 4, US = RP + 4;  // rows 4 words apart from a multiple of 32: no bank conflicts
     constexpr int LPR = NP == 64 ? 16 : 32, NQ = NP / (4 * LPR), JT = RP / 4, PC = RP == 32 ? 128 : 192;
@@ -52,6 +64,7 @@ adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hi
     float* sh = sm;                 // [kRows][HS] dh
     float* su = sh + kRows * HS;    // [kRows][US] u
     float* sb = su + kRows * US;    // [RP][HS] B_a transposed; row j sits at (j % JT) * 4 + j / JT
+    __shared__ float srow[kRows];   // 2^k of each row
     const int tid = threadIdx.x, te = tid >> 3, tj = tid & 7;
     const int lrow = tid / LPR, lcol = tid % LPR;
     pdl_trigger();
@@ -64,13 +77,13 @@ adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hi
     int g = -1;
     auto flush = [&]() {
         if (g < 0 || g >= na) return;
-        float* out = slots + ((int64_t)c + g) * n * r;
+        float* to = slots + ((int64_t)c + g) * n * r;
 #pragma unroll
         for (int a = 0; a < NE; ++a)
 #pragma unroll
             for (int b = 0; b < NJ; ++b) {
                 const int e = NE * te + a, j = NJ * tj + b;
-                if (e < n && j < r) out[e * r + j] = acc[a][b];
+                if (e < n && j < r) to[e * r + j] = acc[a][b];
             }
     };
     for (int blk = b0; blk < b1; ++blk) {
@@ -136,23 +149,47 @@ adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hi
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             const int q = lrow + kThreads / LPR * i;
+            float up = 1.f;
+            if (out.dhs) {  // the row's largest value sets its exponent
+                float top = 0.f;
+#pragma unroll
+                for (int c = 0; c < NQ; ++c)
+                    top = fmaxf(fmaxf(fmaxf(top, fabsf(v[i][c].x)), fabsf(v[i][c].y)), fmaxf(fabsf(v[i][c].z), fabsf(v[i][c].w)));
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int k = fit_exponent(top, kRowExponent);
+                up = ldexpf(1.f, k);
+                if (lcol == 0) { srow[q] = up; out.rinv[p0 + q] = ldexpf(1.f, -k); }
+            }
 #pragma unroll
             for (int c = 0; c < NQ; ++c) {
                 const int e = 4 * (lcol + LPR * c);
                 *reinterpret_cast<float4*>(sh + q * HS + e) = v[i][c];
-                if (e < nk) {
+                if (out.dhs && e < nk) {
+                    __half p[4][2];
+                    split2h(up * v[i][c].x, p[0]);
+                    split2h(up * v[i][c].y, p[1]);
+                    split2h(up * v[i][c].z, p[2]);
+                    split2h(up * v[i][c].w, p[3]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const __half2 lo(p[0][k], p[1][k]), hi(p[2][k], p[3][k]);
+                        *reinterpret_cast<uint2*>(out.dhs + ((int64_t)k * mp + p0 + q) * nk + e) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                    }
+                }
+                if (out.dhp && e < nk) {
                     __nv_bfloat16 p[4][3];
                     split3(v[i][c].x, p[0]);
                     split3(v[i][c].y, p[1]);
                     split3(v[i][c].z, p[2]);
                     split3(v[i][c].w, p[3]);
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        if (k < planes) {
-                            const __nv_bfloat162 lo(p[0][k], p[1][k]), hi(p[2][k], p[3][k]);
-                            *reinterpret_cast<uint2*>(dhp + ((int64_t)k * mp + p0 + q) * nk + e) =
-                                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                        }
+                    for (int k = 0; k < 3; ++k) {
+                        const __nv_bfloat162 lo(p[0][k], p[1][k]), hi(p[2][k], p[3][k]);
+                        *reinterpret_cast<uint2*>(out.dhp + ((int64_t)k * mp + p0 + q) * nk + e) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                    }
                 }
             }
         }
@@ -174,23 +211,27 @@ adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hi
                 }
             }
             const float s = scale[g];
-            __nv_bfloat16* o = dup + (int64_t)(p0 + q) * PC + part * JT;
+            auto store = [&](__nv_bfloat16* o, float up) {
 #pragma unroll
-            for (int b = 0; b < JT; b += 8) {
-                __nv_bfloat16 p[8][3];
+                for (int b = 0; b < JT; b += 8) {
+                    __nv_bfloat16 p[8][3];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) split3(s * t[b + c], p[c]);
+                    for (int c = 0; c < 8; ++c) split3(s * t[b + c] * up, p[c]);
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    uint32_t u[4];
+                    for (int k = 0; k < 3; ++k) {
+                        uint32_t u[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const __nv_bfloat162 two(p[2 * c][k], p[2 * c + 1][k]);
-                        u[c] = *reinterpret_cast<const uint32_t*>(&two);
+                        for (int c = 0; c < 4; ++c) {
+                            const __nv_bfloat162 two(p[2 * c][k], p[2 * c + 1][k]);
+                            u[c] = *reinterpret_cast<const uint32_t*>(&two);
+                        }
+                        *reinterpret_cast<uint4*>(o + k * RP + b) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                    *reinterpret_cast<uint4*>(o + k * RP + b) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
-            }
+            };
+            const int64_t at = (int64_t)(p0 + q) * PC + part * JT;
+            store(out.dup + at, 1.f);
+            if (out.dus && part * JT < (r + 15) / 16 * 16) store(out.dus + at, srow[q]);  // dx stops at whole 16 ranks
         }
         float part[NE][NJ];
 #pragma unroll
@@ -255,13 +296,16 @@ struct AdxShared {
     int abort_flag;
 };
 
-// ND: columns of d at a time; NC: 64-column chunks of dh; RP: padded rank. An MMA with M = 128 took 120 to 140 cycles
-// here whatever its N (the 128 rows of A are read again), so N is 256 where the two accumulators and the ring allow it:
-// 128 columns for 256 rows at a time measured 152 us against 132 us (65536 rows, d 4096, n 64, rank 16).
+// ND: columns of d at a time; NC: 64-column chunks of dh; RP: padded rank. N is 256 where the two accumulators and the
+// ring allow it: 128 columns for 256 rows at a time measured 152 us against 132 us (65536 rows, d 4096, n 64, rank 16,
+// two bf16 parts). Both the MMAs and the drain count: 13 more MMAs a unit cost 74 us there, and loads of the column
+// factors inside the drain's loop 36 us.
 template <int ND, int NC, int RP>
 struct AdxTile {
     static constexpr int DH_BYTES = 2 * NC * 16384;             // [plane][chunk] of 128 rows of 128 bytes
-    static constexpr int DU_CHUNKS = RP / 32;                   // [hi | lo] in one chunk for rank 32, else one each
+    static constexpr int DU_ALL = RP == 32 ? 2 : 3;             // du's parts: [p0 | p1], [p2 | -] for rank 32, else a chunk each
+    static constexpr bool STREAM = NC == 4;                     // p2 comes through the ring, behind A_a
+    static constexpr int DU_CHUNKS = STREAM ? DU_ALL - 1 : DU_ALL;
     static constexpr int A_BYTES = DH_BYTES + DU_CHUNKS * 16384;
     static constexpr int SLOT = ND * 128;                       // 64 columns of a part of W_r, or A_a
     static constexpr int OUT_BYTES = 8 * 32 * 64 * 2;
@@ -270,8 +314,13 @@ struct AdxTile {
     static constexpr size_t SMEM = 1024 + A_BYTES + SLOTS * SLOT + OUT_BYTES + sizeof(AdxShared);
     static_assert(SLOTS >= 2, "a slot is filled while another is read");
     static_assert(2 * ND <= 512, "two accumulators fit the TMEM");
-    static_assert(ND / 64 * RP * 128 <= SLOT, "A_a fits a slot");
+    static_assert(ND / 64 * RP * 128 <= SLOT && SLOT >= 16384, "A_a and a chunk of du fit a slot");
 };
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
 
 // One unit = 128 grouped rows x ND columns of d; the units of a row tile follow one another, and the line of units is
 // cut evenly over the CTAs.
@@ -280,7 +329,8 @@ template <int ND, int NC, int RP>
 __global__ void __launch_bounds__(adx::kThreads, 1)
 adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_constant__ CUtensorMap map_du,
                       const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, int d, int r,
-                      int na, AdapterPlan plan, __nv_bfloat16* __restrict__ dx) {
+                      int na, AdapterPlan plan, const float* __restrict__ rinv, const __nv_bfloat16* __restrict__ cinv,
+                      __nv_bfloat16* __restrict__ dx) {
     using namespace adx;
     using T = AdxTile<ND, NC, RP>;
     constexpr int SLOTS = T::SLOTS;
@@ -356,14 +406,16 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                 }
             }
             if (cnt == 0) continue;
-            // slots in order: both parts of each chunk of W_r, then A_a
-            for (int c = 0; c < 2 * NC + (g < na ? 1 : 0); ++c) {
+            // slots in order: both parts of each chunk of W_r, then A_a, then (STREAM) the third part of du
+            for (int c = 0; c < 2 * NC + (g < na ? (T::STREAM ? 2 : 1) : 0); ++c) {
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag));
                 if (!ok) break;
                 uint8_t* st = ring + stage * T::SLOT;
-                if (leader) ptx::mbar_expect_tx(&sh->full[stage], c < 2 * NC ? ND * 128 : ND / 64 * RP * 128);
+                if (leader) ptx::mbar_expect_tx(&sh->full[stage], c < 2 * NC ? ND * 128 : c == 2 * NC ? ND / 64 * RP * 128 : 16384);
                 __syncwarp();
-                if (c < 2 * NC) {
+                if (c > 2 * NC) {
+                    ptx::tma_load_2d_if(leader, st, &map_du, &sh->full[stage], 64 * (T::DU_ALL - 1), p0);
+                } else if (c < 2 * NC) {
                     ptx::tma_load_3d_if(leader, st, &map_w, &sh->full[stage], 64 * (c >> 1), d0, c & 1);
                 } else {
 #pragma unroll
@@ -374,7 +426,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
             }
         }
     } else if (warp == 1) {
-        constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, ND);
+        constexpr uint32_t idesc = ptx::idesc_f16_f32(128, ND), idesc_u = ptx::idesc_bf16_f32(128, ND) | kIdescBMn;
         int stage = 0, buf = 0;
         uint32_t phase = 0, aphase = 0, bphase = 0;
         int64_t held = -1;
@@ -413,15 +465,26 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                     }
                 } else {
                     const uint32_t ua = ptx::smem_u32(su);
-                    const uint64_t uhi = ptx::sw128_kmajor_desc(ua);
-                    const uint64_t ulo = RP == 32 ? uhi + 4 : ptx::sw128_kmajor_desc(ua + 16384);
+                    const uint64_t u0 = ptx::sw128_kmajor_desc(ua);
+                    const uint64_t u1 = RP == 32 ? u0 + 4 : ptx::sw128_kmajor_desc(ua + 16384);
                     const uint64_t bd = sw128_mnmajor_desc(st, RP * 128);
+                    uint64_t u2 = ptx::sw128_kmajor_desc(ua + (T::DU_ALL - 1) * 16384);
+                    const int held = stage;
+                    if (T::STREAM) {
+                        if (++stage == SLOTS) { stage = 0; phase ^= 1u; }
+                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh->full[stage], phase, abort_flag));
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        u2 = ptx::sw128_kmajor_desc(ptx::smem_u32(ring + stage * T::SLOT));
+                    }
 #pragma unroll
                     for (int k = 0; k < RP / 16; ++k)
                         if (16 * k < r) {
-                            ptx::umma_bf16_if(leader, acc, uhi + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
-                            ptx::umma_bf16_if(leader, acc, ulo + 2 * k, bd + 128 * k, idesc | kIdescBMn, 1u);
+                            ptx::umma_bf16_if(leader, acc, u0 + 2 * k, bd + 128 * k, idesc_u, 1u);
+                            ptx::umma_bf16_if(leader, acc, u1 + 2 * k, bd + 128 * k, idesc_u, 1u);
+                            ptx::umma_bf16_if(leader, acc, u2 + 2 * k, bd + 128 * k, idesc_u, 1u);
                         }
+                    if (T::STREAM) ptx::umma_commit_if(leader, &sh->empty[held]);
                 }
                 ptx::umma_commit_if(leader, &sh->empty[stage]);
                 if (++stage == SLOTS) { stage = 0; phase ^= 1u; }
@@ -439,6 +502,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
         int64_t held = -1;
         int g = 0, p0 = 0, cnt = 0;
         int32_t rows[PIECES];  // the rows that this lane stores: quad rows lane / PIECES + (32 / PIECES) i
+        float rs = 1.f;        // 2^-k of this lane's row of the accumulator
         for (int64_t u = lo; u < hi; ++u) {
             const int64_t tile = u / ndc;
             const int d0 = (int)(u - tile * ndc) * ND;
@@ -450,12 +514,17 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                     const int q = quad * 32 + lane / PIECES + 32 / PIECES * i;
                     rows[i] = q < cnt ? plan.perm[p0 + q] : -1;
                 }
+                if (quad * 32 + lane < cnt) rs = rinv[p0 + quad * 32 + lane];
             }
             if (cnt == 0) continue;
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sh->tfull[buf], bphase, abort_flag))) break;
             ptx::tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * ND + col0);
             const bool any = quad * 32 < cnt;
+            uint4 cs[ND / 128];  // 2^-k of the eight columns that this lane stores
+#pragma unroll
+            for (int w = 0; w < ND / 128; ++w)
+                cs[w] = *reinterpret_cast<const uint4*>(cinv + d0 + col0 + 64 * w + 8 * (lane % PIECES));
 #pragma unroll
             for (int w = 0; w < ND / 2; w += 64) {
                 if (any) {
@@ -469,7 +538,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                         uint32_t o[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[8 * p + 2 * q]), __uint_as_float(v[8 * p + 2 * q + 1]));
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(rs * __uint_as_float(v[8 * p + 2 * q]), rs * __uint_as_float(v[8 * p + 2 * q + 1]));
                             o[q] = *reinterpret_cast<const uint32_t*>(&b);
                         }
                         const int at = p ^ (lane & 7);
@@ -487,7 +556,9 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                     for (int i = 0; i < PIECES; ++i) {
                         const int q = lane / PIECES + 32 / PIECES * i;
                         const int at = piece ^ (q & 7);
-                        const uint4 t = *reinterpret_cast<const uint4*>(mine + (q * PIECES + at) * 16);
+                        uint4 t = *reinterpret_cast<const uint4*>(mine + (q * PIECES + at) * 16);
+                        t = make_uint4(mul_bf16x2(t.x, cs[w / 64].x), mul_bf16x2(t.y, cs[w / 64].y), mul_bf16x2(t.z, cs[w / 64].z),
+                                       mul_bf16x2(t.w, cs[w / 64].w));
                         if (rows[i] >= 0 && col < d) *reinterpret_cast<uint4*>(dx + (int64_t)rows[i] * d + col) = t;
                     }
                 }
@@ -785,9 +856,10 @@ rows_contract_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_
 // ---------------------------------------------------------------- host side
 struct AgtWs {
     AdapterPlan plan;
-    __nv_bfloat16 *wparts;  // [2, d, nk]
-    __nv_bfloat16 *dhp;     // [3, m_pad, nk]
-    __nv_bfloat16 *dup;     // [m_pad, pc]
+    __half* wscaled;        // [2, d, nk]
+    __nv_bfloat16* cinv;    // [d], padded to 256
+    __nv_bfloat16* ascaled; // [na r, d]
+    SplitOut split;
     float *slots;           // [grid + na][n, r]
     float *part;            // [2 kNumSMs][64][256]
     int32_t *tickets;       // one per unit of the two contractions
@@ -816,9 +888,14 @@ static size_t agt_layout(int64_t m, int d, int n, int r, int na, AgtWs* w, char*
     size_t off = adapter_plan_layout(m, na, w ? &w->plan : nullptr, base);
     auto take = [&](size_t bytes) { char* p = base + off; off += (bytes + 255) & ~size_t(255); return p; };
     char* p;
-    p = take((size_t)2 * d * s.nk * 2);                         if (w) w->wparts = (__nv_bfloat16*)p;
-    p = take((size_t)3 * s.mp * s.nk * 2);                      if (w) w->dhp = (__nv_bfloat16*)p;
-    p = take((size_t)s.mp * s.pc * 2);                          if (w) w->dup = (__nv_bfloat16*)p;
+    p = take((size_t)2 * d * s.nk * 2);                         if (w) w->wscaled = (__half*)p;
+    p = take((size_t)(d + 255) / 256 * 256 * 2);                if (w) w->cinv = (__nv_bfloat16*)p;
+    p = take((size_t)na * r * d * 2);                           if (w) w->ascaled = (__nv_bfloat16*)p;
+    p = take((size_t)3 * s.mp * s.nk * 2);                      if (w) w->split.dhp = (__nv_bfloat16*)p;
+    p = take((size_t)s.mp * s.pc * 2);                          if (w) w->split.dup = (__nv_bfloat16*)p;
+    p = take((size_t)2 * s.mp * s.nk * 2);                      if (w) w->split.dhs = (__half*)p;
+    p = take((size_t)s.mp * s.pc * 2);                          if (w) w->split.dus = (__nv_bfloat16*)p;
+    p = take((size_t)s.mp * 4);                                 if (w) w->split.rinv = (float*)p;
     p = take((size_t)(asp::kGrid + na) * n * r * 4);            if (w) w->slots = (float*)p;
     p = take((size_t)2 * kNumSMs * 64 * rct::BD * 4);           if (w) w->part = (float*)p;
     p = take((size_t)(s.tickets_a + s.tickets_w) * 4);          if (w) w->tickets = (int32_t*)p;
@@ -827,13 +904,13 @@ static size_t agt_layout(int64_t m, int d, int n, int r, int na, AgtWs* w, char*
 
 template <int ND, int NC, int RP>
 static cudaError_t launch_adx(const CUtensorMap& mdh, const CUtensorMap& mdu, const CUtensorMap& mw,
-                              const CUtensorMap& ma, int d, int r, int na, const AdapterPlan& plan,
-                              __nv_bfloat16* dx, cudaStream_t stream) {
+                              const CUtensorMap& ma, int d, int r, int na, const AgtWs& w, __nv_bfloat16* dx,
+                              cudaStream_t stream) {
     constexpr size_t smem = AdxTile<ND, NC, RP>::SMEM;
     const cudaError_t e = need_smem<adapters_dx_tc_kernel<ND, NC, RP>>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(adapters_dx_tc_kernel<ND, NC, RP>, dim3(kNumSMs), dim3(adx::kThreads), smem, stream, mdh, mdu,
-                      mw, ma, d, r, na, plan, dx);
+                      mw, ma, d, r, na, w.plan, w.split.rinv, w.cinv, dx);
 }
 
 template <int C>
@@ -849,12 +926,12 @@ static cudaError_t launch_rct(const CUtensorMap& mx, const CUtensorMap& mg, cons
 
 template <int NE, int NJ, int RP>
 static cudaError_t launch_split(const float* dh, const float* hidden, const __nv_bfloat16* b, const float* scale, int n,
-                                int r, int na, const AgtShape& s, const AgtWs& w, int planes, cudaStream_t stream) {
+                                int r, int na, const AgtShape& s, const AgtWs& w, cudaStream_t stream) {
     constexpr size_t smem = sizeof(float) * ((size_t)(asp::kRows + RP) * (NE * 32 + 4) + (size_t)asp::kRows * (RP + 4));
     const cudaError_t e = need_smem<adapters_split_kernel<NE, NJ, RP>>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(adapters_split_kernel<NE, NJ, RP>, dim3(asp::kGrid), dim3(asp::kThreads), smem, stream, dh, hidden,
-                      b, scale, n, r, na, w.plan, s.nk, planes, s.mp, w.dhp, w.dup, w.slots);
+                      b, scale, n, r, na, w.plan, s.nk, s.mp, w.split, w.slots);
 }
 
 static cudaError_t launch_adapters_grad_tc(const float* dh, const __nv_bfloat16* x, const float* w_r,
@@ -866,11 +943,13 @@ static cudaError_t launch_adapters_grad_tc(const float* dh, const __nv_bfloat16*
     AgtWs w;
     agt_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
     PrepExtra extra = {};
-    extra.w_r = w_r; extra.d = d; extra.n = n; extra.nk = s.nk; extra.parts = 2; extra.wparts = dx ? w.wparts : nullptr;
+    extra.w_r = w_r; extra.d = d; extra.n = n; extra.nk = s.nk; extra.wscaled = dx ? w.wscaled : nullptr;
+    extra.cinv = w.cinv; extra.a = a; extra.ascaled = w.ascaled; extra.arows = na * r;
     cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, w.tickets, s.tickets_a + s.tickets_w, extra, stream);
     if (e != cudaSuccess) return e;
-    const int planes = dw_r ? 3 : 2;
-#define MOE_SPLIT(NE, NJ, RP) e = launch_split<NE, NJ, RP>(dh, hidden, b, scale, n, r, na, s, w, planes, stream)
+    if (!dx) { w.split.dhs = nullptr; w.split.dus = nullptr; w.split.rinv = nullptr; }
+    if (!dw_r) w.split.dhp = nullptr;
+#define MOE_SPLIT(NE, NJ, RP) e = launch_split<NE, NJ, RP>(dh, hidden, b, scale, n, r, na, s, w, stream)
 #define MOE_SPLIT_R(NE) do { if (r <= 16) MOE_SPLIT(NE, 2, 32); else if (r <= 32) MOE_SPLIT(NE, 4, 32); else MOE_SPLIT(NE, 8, 64); } while (0)
     if (n <= 64) MOE_SPLIT_R(2);
     else if (n <= 128) MOE_SPLIT_R(4);
@@ -880,16 +959,16 @@ static cudaError_t launch_adapters_grad_tc(const float* dh, const __nv_bfloat16*
     if (e != cudaSuccess) return e;
     CUtensorMap mx, mg, ma, mw, mdh, mdu, mpw, mpa;
     if (!map_2d(&mx, x, (uint64_t)m, (uint64_t)d, 32) || !map_2d(&mg, x, (uint64_t)m, (uint64_t)d, 1) ||
-        !map_3d(&mpa, w.dup, 1, (uint64_t)s.mp, (uint64_t)s.pc, rct::BK) ||
-        !map_3d(&mpw, w.dhp, 3, (uint64_t)s.mp, (uint64_t)s.nk, rct::BK) ||
-        !map_3d(&ma, a, (uint64_t)na, (uint64_t)r, (uint64_t)d, (uint32_t)s.rp) ||
-        !map_3d(&mdh, w.dhp, 2, (uint64_t)s.mp, (uint64_t)s.nk, 128) ||
-        !map_2d(&mdu, w.dup, (uint64_t)s.mp, (uint64_t)s.pc, 128))
+        !map_3d(&mpa, w.split.dup, 1, (uint64_t)s.mp, (uint64_t)s.pc, rct::BK))
         return cudaErrorInvalidValue;
     if (dx) {
         const int nd = n <= 128 ? 256 : 128;
-        if (!map_3d(&mw, w.wparts, 2, (uint64_t)d, (uint64_t)s.nk, (uint32_t)nd)) return cudaErrorInvalidValue;
-#define MOE_ADX(ND, NC, RP) e = launch_adx<ND, NC, RP>(mdh, mdu, mw, ma, d, r, na, w.plan, dx, stream)
+        if (!map_3d(&mw, w.wscaled, 2, (uint64_t)d, (uint64_t)s.nk, (uint32_t)nd) ||
+            !map_3d(&ma, w.ascaled, (uint64_t)na, (uint64_t)r, (uint64_t)d, (uint32_t)s.rp) ||
+            !map_3d(&mdh, w.split.dhs, 2, (uint64_t)s.mp, (uint64_t)s.nk, 128) ||
+            !map_2d(&mdu, w.split.dus, (uint64_t)s.mp, (uint64_t)s.pc, 128))
+            return cudaErrorInvalidValue;
+#define MOE_ADX(ND, NC, RP) e = launch_adx<ND, NC, RP>(mdh, mdu, mw, ma, d, r, na, w, dx, stream)
         if (n <= 64) { if (s.rp == 32) MOE_ADX(256, 1, 32); else MOE_ADX(256, 1, 64); }
         else if (n <= 128) { if (s.rp == 32) MOE_ADX(256, 2, 32); else MOE_ADX(256, 2, 64); }
         else { if (s.rp == 32) MOE_ADX(128, 4, 32); else MOE_ADX(128, 4, 64); }
@@ -902,6 +981,7 @@ static cudaError_t launch_adapters_grad_tc(const float* dh, const __nv_bfloat16*
         e = launch_rct<64>(mx, mg, mpa, d, r, na, 0, w.plan, w.part, w.tickets, da, (int64_t)r * d, d, 1, stream);
     if (e != cudaSuccess) return e;
     if (dw_r) {
+        if (!map_3d(&mpw, w.split.dhp, 3, (uint64_t)s.mp, (uint64_t)s.nk, rct::BK)) return cudaErrorInvalidValue;
         e = launch_rct<64>(mx, mg, mpw, d, n, na, 1, w.plan, w.part, w.tickets + s.tickets_a, dw_r, 0, 1, n, stream);
         if (e != cudaSuccess) return e;
     }

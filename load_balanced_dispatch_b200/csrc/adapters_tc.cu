@@ -510,7 +510,7 @@ static cudaError_t launch_router_adapters_tc(const __nv_bfloat16* x, const float
     AtcWs w;
     atc_layout(m, d, n, r, na, &w, static_cast<char*>(workspace));
     PrepExtra extra = {};
-    extra.w_r = w_r; extra.d = d; extra.n = n; extra.parts = 3; extra.wparts = w.wsplit;
+    extra.w_r = w_r; extra.d = d; extra.n = n; extra.wparts = w.wsplit;
     const cudaError_t e = launch_adapter_prep(idx, m, na, w.plan, w.tickets, atc_tiles(m, na) * nct, extra, stream);
     if (e != cudaSuccess) return e;
     CUtensorMap mx, mg, mw, ma;

@@ -177,6 +177,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
            | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
+// The same with fp16 A and B (format 0 in both fields).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+    return idesc_bf16_f32(M, N) & ~((7u << 7) | (7u << 10));
+}
+
 __device__ __forceinline__ void umma_bf16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
     asm volatile(

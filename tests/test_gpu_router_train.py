@@ -602,3 +602,57 @@ def test_calls_that_follow_one_another(m, d, n, r, na, order):
     for f, b in outs:
         for p, q in zip(f + b, first + grads):
             assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("m,d,n,r,na", [(700, 520, 64, 16, 3), (300, 264, 40, 50, 2), (260, 512, 128, 8, 2),
+                                        (300, 200, 100, 64, 3), (515, 392, 256, 16, 4), (140, 128, 200, 40, 2)])
+def test_adapters_backward_dx_keeps_fp32_sums(m, d, n, r, na):
+    # the gradient of a softmax adds up to zero over the experts, so what the columns of W_r have in common cancels in
+    # dx: what is left has to be right to fp32 sums of the products, not to a multiple of the common part
+    i, dh = adapter_inputs(m, d, n, r, na, torch.bfloat16, "mixed", 71)
+    g = gen(72)
+    p = torch.softmax(dh, 1)
+    dh = p * (dh - (p * dh).sum(1, keepdim=True))
+    i["w_r"] = 8 * torch.randn(d, 1, generator=g, device="cuda") + i["w_r"] / 8
+    i["b"] = (i["b"].float() + 1).to(torch.bfloat16)  # B_a's columns have a common part as well
+    dx, _, _, _ = lb.moe_router_adapters_grad(dh, hidden=torch.zeros(m, r, device="cuda"), **i)
+    lb.sync_status()
+    w, a, b, s = (i[k].double() for k in ("w_r", "a", "b", "scale"))
+    dh64 = dh.double()
+    ref, mag = dh64 @ w.T, dh64.abs() @ w.abs().T
+    for q in range(na):
+        rows = (i["adapter_idx"] == q).nonzero()[:, 0]
+        ref[rows] += s[q] * dh64[rows] @ b[q] @ a[q]
+        mag[rows] += s[q] * dh64[rows].abs() @ b[q].abs() @ a[q].abs()
+    assert float((mag / ref.abs().clamp(min=1e-30)).median()) > 50
+    # three products of the parts for each 16 experts and each 16 ranks, an eps each (12 ceil(n / 64) + 12 steps); du is
+    # a sum of n products; what two fp16 parts a side leave out is below 3 * 2^-22, six eps
+    within(dx, ref, 2.0 ** -8 * ref.abs() + (12 * -(-n // 64) + 12 + n + 6) * EPS * mag, "dx")
+
+
+@pytest.mark.parametrize("m,d,n,r,na", [(300, 264, 64, 16, 3), (200, 136, 200, 40, 2)])
+def test_adapters_backward_dx_at_any_scale(m, d, n, r, na):
+    # rows of dlogits and of W_r (which the kernels scale to fit fp16 parts) of very different sizes, some all zero, next
+    # to adapters that are not as large or small as their row of W_r; elements of a row that differ by up to 2^12
+    i, dh = adapter_inputs(m, d, n, r, na, torch.bfloat16, "mixed", 73)
+    g = gen(74)
+
+    def powers(low, high, *shape):
+        return 2.0 ** torch.randint(low, high + 1, shape, generator=g, device="cuda").float()
+    dh = dh * powers(-60, 30, m, 1) * powers(-12, 0, m, n)
+    i["w_r"] = i["w_r"] * powers(-30, 30, d, 1) * powers(-12, 0, d, n)
+    i["a"] = (i["a"].float() * powers(-20, 10, na, r, d)).to(torch.bfloat16)
+    dh[5], dh[17, 1:], i["w_r"][3] = 0, 0, 0
+    dx, _, _, _ = lb.moe_router_adapters_grad(dh, hidden=torch.zeros(m, r, device="cuda"), **i)
+    lb.sync_status()
+    w, a, b, s = (i[k].double() for k in ("w_r", "a", "b", "scale"))
+    dh64 = dh.double()
+    ref, mag = dh64 @ w.T, dh64.abs() @ w.abs().T
+    for q in range(na):
+        rows = (i["adapter_idx"] == q).nonzero()[:, 0]
+        ref[rows] += s[q] * dh64[rows] @ b[q] @ a[q]
+        mag[rows] += s[q] * dh64[rows].abs() @ b[q].abs() @ a[q].abs()
+    # as above, and 2^-39 of the largest product of the row's and the column's values for each of n terms
+    top = n * 2.0 ** -38 * dh64.abs().amax(1)[:, None] * w.abs().amax(1)
+    within(dx, ref, 2.0 ** -8 * ref.abs() + (12 * -(-n // 64) + 12 + n + 6) * EPS * mag + top, "dx")
+    assert not bool(dx[5].any())
