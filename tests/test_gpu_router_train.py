@@ -656,3 +656,40 @@ def test_adapters_backward_dx_at_any_scale(m, d, n, r, na):
     top = n * 2.0 ** -38 * dh64.abs().amax(1)[:, None] * w.abs().amax(1)
     within(dx, ref, 2.0 ** -8 * ref.abs() + (12 * -(-n // 64) + 12 + n + 6) * EPS * mag + top, "dx")
     assert not bool(dx[5].any())
+
+
+@pytest.mark.parametrize("n,r", [(64, 16), (40, 33), (128, 8), (100, 64), (256, 16), (200, 40)])
+@pytest.mark.parametrize("side", ["dlogits", "w_r", "du"])
+def test_adapters_backward_dx_is_exact_where_fp32_is(n, r, side):
+    # pairs of 21-bit integers (times 2^-20) that add up to at most 16: fp32 sums of four pairs are exact, and so is
+    # their bf16 value; parts that keep fewer than 21 bits of dlogits, W_r or du are off by about a unit of the sum
+    m, d = 300, 264
+    g = gen(75 + n)
+    i, dh = adapter_inputs(m, d, n, r, 3, torch.bfloat16, "mixed", 76)
+    i["scale"].fill_(1.0)
+    wide = d if side == "w_r" else m
+    q = torch.randint(2 ** 20, 2 ** 21, (wide, n // 2), generator=g, device="cuda")
+    small = torch.randint(-16, 17, (wide, n // 2), generator=g, device="cuda")
+    pairs = torch.stack([q, small - q], 2).view(wide, -1)  # columns 2 p and 2 p + 1 belong together
+    pick = torch.randint(0, min(n, r) // 2 if side == "du" else n // 2, (m,), generator=g, device="cuda")
+    both = (torch.arange(n // 2, device="cuda") == pick[:, None]).repeat_interleave(2, 1)
+    if side == "w_r":  # a row of dlogits names one pair of each row of W_r
+        dh = both.float()
+        i["w_r"] = pairs.float() * 2.0 ** -20
+        i["adapter_idx"].fill_(-1)
+        want = small[:, pick].T.float() * 2.0 ** -20
+    else:
+        dh = (pairs * both).float() * 2.0 ** -20
+        total = small.gather(1, pick[:, None]).float() * 2.0 ** -20
+        if side == "dlogits":
+            i["w_r"] = torch.ones_like(i["w_r"])
+            i["adapter_idx"].fill_(-1)
+        else:  # du takes the values over one by one, and A_a adds them up
+            i["w_r"] = torch.zeros_like(i["w_r"])
+            i["a"] = torch.ones_like(i["a"])
+            i["b"] = torch.eye(n, r, device="cuda").to(torch.bfloat16).repeat(3, 1, 1)
+            total = total * (i["adapter_idx"] >= 0)[:, None]
+        want = total.expand(m, d)
+    dx, _, _, _ = lb.moe_router_adapters_grad(dh, hidden=torch.zeros(m, r, device="cuda"), **i)
+    lb.sync_status()
+    assert torch.equal(dx.float(), want)
