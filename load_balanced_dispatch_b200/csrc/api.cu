@@ -177,8 +177,8 @@ moe_status moe_router_topk(const void* x, moe_dtype x_dtype, const float* w_r, c
         if (ws_bytes < need || !workspace || !aligned16(workspace))
             return fail(MOE_ERR_WORKSPACE, "moe_router_topk: 16-byte aligned workspace of %zu bytes required", need);
     }
-    return check_launch(launch_router(x, x_dtype, w_r, logits_in, m, d, n, k, (int)fn, renorm_topk, rank_bias,
-                                      probs_out, topk_idx, topk_gate, workspace, stream),
+    const int renorm = renorm_topk && k > 1 ? 1 : 0;  // one pick keeps its score: p / p would be 1 whatever the logits are
+    return check_launch(launch_router(x, x_dtype, w_r, logits_in, m, d, n, k, (int)fn, renorm, rank_bias, probs_out, topk_idx, topk_gate, workspace, stream),
                         "moe_router_topk");
 }
 

@@ -87,8 +87,8 @@ static float add_f32(float a, float b) {
  *   key: with a bias b: fp32(fp32(score) + b); softmax without bias: h;
  *        sigmoid without bias: rho.
  *   top-k by key, ties to the lowest expert index, listed best first.
- *   gate: sigmoid -> rho_sel; softmax -> p_sel, or (renorm) p_sel / sum of
- *         the selected p, i.e. a softmax over the selected logits.
+ *   gate: sigmoid -> rho_sel; softmax -> p_sel, or (renorm and k >= 2) p_sel / sum
+ *         of the selected p, i.e. a softmax over the selected logits.
  *   margin[i] = key of the k-th pick minus key of the (k+1)-th best (inf if k == n).
  */
 int orc_router(const float* x, const float* w_r, const float* logits_in, int64_t m, int d, int n, int k,
@@ -131,7 +131,7 @@ int orc_router(const float* x, const float* w_r, const float* logits_in, int64_t
         for (int r = 0; r < k; ++r) {
             topk_idx[i * k + r] = sel[r];
             double g = p[sel[r]];
-            if (fn == ORC_SOFTMAX && renorm) g = p[sel[r]] / selsum;
+            if (fn == ORC_SOFTMAX && renorm && k > 1) g = p[sel[r]] / selsum;
             topk_gate[i * k + r] = g;
         }
         if (probs_out) for (int j = 0; j < n; ++j) probs_out[i * n + j] = p[j];

@@ -693,3 +693,56 @@ def test_adapters_backward_dx_is_exact_where_fp32_is(n, r, side):
     dx, _, _, _ = lb.moe_router_adapters_grad(dh, hidden=torch.zeros(m, r, device="cuda"), **i)
     lb.sync_status()
     assert torch.equal(dx.float(), want)
+
+
+# ---------------------------------------------------------------- the gates that the router gives and their gradient
+@pytest.mark.parametrize("m,d,n,dtype,probs", [
+    (300, 0, 64, None, True), (200, 0, 256, None, False), (517, 768, 128, "bf16", True), (20000, 64, 64, "bf16", True),
+    (400, 128, 100, "bf16", False), (259, 128, 256, "bf16", True), (100, 64, 8, "fp32", True)])
+def test_one_pick_keeps_its_score_when_renormalising(m, d, n, dtype, probs):
+    # renorm_topk is for two picks and more: one pick's gate is its softmax score, on every path of the router
+    g = gen(m + n)
+    if dtype is None:
+        x = w = None
+        kw = dict(logits_in=torch.randn(m, n, generator=g, device="cuda"))
+    else:
+        x = torch.randn(m, d, generator=g, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+        w = torch.randn(d, n, generator=g, device="cuda") / d ** 0.5
+        kw = {}
+    idx, gate, p = lb.moe_router_topk(x, w, n, 1, renorm_topk=1, want_probs=probs, **kw)
+    idx0, gate0, _ = lb.moe_router_topk(x, w, n, 1, renorm_topk=0, want_probs=probs, **kw)
+    lb.sync_status()
+    assert torch.equal(idx, idx0) and torch.equal(gate, gate0)
+    if probs:
+        assert torch.equal(gate, p.gather(1, idx.long()))
+
+
+@pytest.mark.parametrize("fn,renorm,k", [(0, 0, 1), (0, 1, 1), (0, 0, 3), (0, 1, 3), (1, 0, 2), (1, 1, 1)])
+def test_gate_gradient_by_differences_of_the_router(fn, renorm, k):
+    # sum_r dgate_r gate_r with the gates that moe_router_topk itself gives; the bias keeps the picks fixed
+    m, n, step = 200, 16, 2.0 ** -7
+    g = gen(91)
+    h = torch.randn(m, n, generator=g, device="cuda")
+    v = torch.randn(m, n, generator=g, device="cuda").clamp(-2, 2)
+    dgate = torch.randn(m, k, generator=g, device="cuda")
+    bias = torch.zeros(n, device="cuda")
+    bias[:k] = torch.arange(k, 0, -1, device="cuda") * 4.0
+    cuts = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+
+    def gates(logits):
+        idx, gate, _ = lb.moe_router_topk(None, None, n, k, fn, renorm, rank_bias=bias, logits_in=logits)
+        assert torch.equal(idx, torch.arange(k, device="cuda", dtype=torch.int32).expand(m, k))
+        return idx.contiguous(), gate
+    idx, gate = gates(h)
+    out = lb.moe_router_loss(h, idx, cuts, None, fn, alpha=0.0)
+    dh = lb.moe_router_loss_grad(h, idx, cuts, out["counts"], out["tokens"], None, fn, alpha=0.0, dgate=dgate,
+                                 renorm_topk=renorm)
+    diff = ((gates(h + step * v)[1].double() - gates(h - step * v)[1].double()) / (2 * step) * dgate).sum(1)
+    lb.sync_status()
+    # a gate is off by 16 eps of itself on each side; a score's third derivative along v is at most 8 |v|_inf^3 of its
+    # weight (a softmax's is p times a cubic in the centred steps, |v_j - mean| <= 2 |v|_inf, with coefficients 1, 3, 2:
+    # at most 48 |v|^3 p), step^2 / 6 of it remains
+    mag = (gate.double() * dgate.abs()).sum(1)
+    bound = 16 * EPS * mag / step + 48 * 8 * step ** 2 / 6 * mag + 64 * EPS * (dh.abs() * v.abs()).sum(1) + 1e-9
+    assert bool(((diff - (dh.double() * v).sum(1)).abs() <= bound).all())
+    assert fn == 1 or renorm == 0 or k > 1 or bool((dh.abs().sum(1) > 0).any())

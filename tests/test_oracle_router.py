@@ -141,3 +141,11 @@ def test_margin_definition():
     assert margin[0] == pytest.approx(0.25)
     _, _, _, margin_all = oracle.router(None, None, 1, 0, 4, 4, logits_in=logits)
     assert math.isinf(margin_all[0])
+
+
+def test_one_pick_keeps_its_score_when_renormalising():
+    logits = np.array([[0.3, -1.2, 2.5, 0.0]], dtype=np.float32)
+    p = np.exp(logits[0].astype(np.float64))
+    for renorm in (0, 1):
+        _, idx, gate, _ = oracle.router(None, None, 1, 0, 4, 1, renorm=renorm, logits_in=logits)
+        assert idx[0, 0] == 2 and gate[0, 0] == pytest.approx(p[2] / p.sum(), rel=1e-12)
