@@ -14,8 +14,8 @@ import torch
 from . import (MOE_QB_MIDPOINT, MOE_QB_STEP, MOE_SIGMOID, MOE_SOFTMAX, moe_balance_assign, moe_balance_stats,
                moe_capacity_slots, moe_combine, moe_combine_grad, moe_dispatch_tokens, moe_expert_ffn,
                moe_expert_ffn_combine, moe_expert_ffn_gather, moe_router_adapters, moe_router_adapters_grad,
-               moe_router_adapters_grad_workspace_size, moe_router_adapters_workspace_size, moe_router_loss,
-               moe_router_loss_grad, moe_router_loss_workspace_size, moe_router_prepare, moe_router_topk, lib)
+               moe_router_adapters_workspace_size, moe_router_loss, moe_router_loss_grad, moe_router_prepare,
+               moe_router_topk, lib)
 
 
 @dataclass
@@ -232,19 +232,15 @@ class MoELayer:
         s, b, w, ad = self.shape, self.buf, self.w, self.adapters
         fn = MOE_SOFTMAX if s.score_fn == "softmax" else MOE_SIGMOID
         coef = dict(token_mask=token_mask, score_fn=fn, alpha=s.alpha, alpha_seq=alpha_seq, z_coef=z_coef, stream=stream)
-        na, r = ad["a"].shape[:2]
-        nseq = seq_offsets.shape[0] - 1
-        for key, size in (("loss", moe_router_loss_workspace_size(s.m, s.n, nseq)),
-                          ("adapters_grad", moe_router_adapters_grad_workspace_size(s.m, s.d, s.n, r, na, s.dtype))):
-            if key not in self.ws or self.ws[key].numel() < size:
-                self.ws[key] = torch.empty((size,), dtype=torch.uint8, device=self.device)
+        # each call makes its workspace on the stream that it runs on: the sizes follow the batch's sequences, and one
+        # kept here could be replaced (and its memory given away) while a call on another stream, or a captured one, uses it
         dybuf, dgate = moe_combine_grad(dy, b["ybuf"], b["dest_row"], b["topk_gate"], stream=stream)
-        out = moe_router_loss(b["logits"], b["topk_idx"], seq_offsets, workspace=self.ws["loss"], **coef)
+        out = moe_router_loss(b["logits"], b["topk_idx"], seq_offsets, **coef)
         dlogits = moe_router_loss_grad(b["logits"], b["topk_idx"], seq_offsets, out["counts"], out["tokens"], dloss=dloss,
                                        dgate=dgate, renorm_topk=s.renorm_topk, **coef)
         dx, da, db, dw_r = moe_router_adapters_grad(
             dlogits, x, w["w_r"], ad["a"], ad["b"], ad["adapter_idx"], ad["scale"], b["hidden"], want_dx=want_dx,
-            want_dw_r=want_dw_r, workspace=self.ws["adapters_grad"], stream=stream)
+            want_dw_r=want_dw_r, stream=stream)
         return dict(out, da=da, db=db, dw_r=dw_r, dx=dx, dybuf=dybuf, dgate=dgate, dlogits=dlogits)
 
     def enable_global_stats(self, m_total: int, group=None) -> None:

@@ -127,3 +127,47 @@ def test_router_backward_shapes_and_pieces():
     dx, da, db, _ = lb.moe_router_adapters_grad(out["dlogits"], x, layer.w["w_r"], hidden=hidden, **ad)
     for key, want in (("dx", dx), ("da", da), ("db", db)):
         assert torch.equal(out[key], want), key
+
+
+def test_router_backward_on_a_side_stream_with_growing_batches():
+    # the sequences grow from call to call, other work allocates and writes on the main stream, nothing waits in between
+    layer, x, ad, dy = make("global", r=16, **GLOBAL)
+    layer.enable_adapters(**ad)
+    layer.forward(x)
+    cuts = [torch.linspace(0, 2304, nseq + 1, device="cuda").to(torch.int32) for nseq in (1, 7, 300, 2000)]
+    want = [layer.router_backward(x, dy, c, alpha_seq=1e-3, want_dw_r=True) for c in cuts]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        for c in cuts:
+            got.append(layer.router_backward(x, dy, c, alpha_seq=1e-3, want_dw_r=True, stream=side))
+            for size in (1 << 16, 1 << 20, 1 << 23):
+                torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    torch.cuda.synchronize()
+    lb.sync_status()
+    for j, out in enumerate(got):
+        for key in out:
+            assert torch.equal(out[key], want[j % len(cuts)][key]), (key, j)
+
+
+def test_router_backward_captured_before_a_larger_batch():
+    # a captured backward keeps its memory when a later call has more sequences
+    layer, x, ad, dy = make("tiny", **TINY)
+    layer.enable_adapters(**ad)
+    layer.forward(x)
+    few = torch.tensor([0, 60, 192], dtype=torch.int32, device="cuda")
+    many = torch.arange(0, 193, dtype=torch.int32, device="cuda")
+    want = layer.router_backward(x, dy, few, alpha_seq=1e-2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer.router_backward(x, dy, few, alpha_seq=1e-2)
+    eager = layer.router_backward(x, dy, many, alpha_seq=1e-2)
+    keep = {key: t.clone() for key, t in eager.items() if t is not None}
+    graph.replay()
+    torch.cuda.synchronize()
+    for key, t in want.items():
+        assert t is None or torch.equal(got[key], t), key
+    for key, t in keep.items():
+        assert torch.equal(eager[key], t), key

@@ -1,0 +1,43 @@
+"""The layer with adapters beside its router: what it asks of the entry points, and its refusals (host only: the entry
+points are stood in for)."""
+import pytest
+import torch
+
+from load_balanced_dispatch_b200 import layer as L
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Stands in for the entry points that router_backward calls; the list of (name, keyword arguments)."""
+    seen = []
+    t = torch.zeros(1)
+    gives = dict(moe_combine_grad=(t, t), moe_router_loss=dict(loss=t, counts=t, tokens=t, f=t, P=t),
+                 moe_router_loss_grad=t, moe_router_adapters_grad=(t, t, t, None))
+    for name, out in gives.items():
+        monkeypatch.setattr(L, name, lambda *a, _n=name, _o=out, **kw: (seen.append((_n, kw)), _o)[1])
+    return seen
+
+
+def bare_layer(m=64, d=32, n=8, k=2, dtype=torch.bfloat16):
+    """A layer after a forward with adapters, without its device buffers."""
+    layer = object.__new__(L.MoELayer)
+    layer.shape = L.LayerShape(m=m, d=d, n=n, k=k, d_ff=16, dtype=dtype)
+    layer.device = torch.device("cpu")
+    layer.w = dict(w_r=torch.zeros(d, n))
+    layer.buf = {key: torch.zeros(1) for key in ("ybuf", "dest_row", "topk_gate", "logits", "topk_idx", "hidden")}
+    layer.ws, layer.global_stats = {}, None
+    layer.adapters = dict(a=torch.zeros(3, 4, d), b=torch.zeros(3, n, 4), scale=torch.zeros(3),
+                          adapter_idx=torch.zeros(m, dtype=torch.int32))
+    return layer
+
+
+def test_router_backward_leaves_workspaces_to_the_stream_of_each_call(calls):
+    # a workspace that the layer keeps would be made on the current stream and replaced when a batch has more sequences,
+    # while `stream` may still use it
+    layer, side = bare_layer(), object()
+    for nseq in (1, 5, 500):
+        layer.router_backward(torch.zeros(64, 32), torch.zeros(64, 32), torch.zeros(nseq + 1, dtype=torch.int32), stream=side)
+    assert [name for name, _ in calls] == ["moe_combine_grad", "moe_router_loss", "moe_router_loss_grad",
+                                           "moe_router_adapters_grad"] * 3
+    assert all(kw["stream"] is side and kw.get("workspace") is None for _, kw in calls)
+    assert not layer.ws
