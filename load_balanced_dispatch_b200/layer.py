@@ -15,7 +15,7 @@ from . import (MOE_QB_MIDPOINT, MOE_QB_STEP, MOE_SIGMOID, MOE_SOFTMAX, moe_balan
                moe_capacity_slots, moe_combine, moe_combine_grad, moe_dispatch_tokens, moe_expert_ffn,
                moe_expert_ffn_combine, moe_expert_ffn_gather, moe_router_adapters, moe_router_adapters_grad,
                moe_router_adapters_workspace_size, moe_router_loss, moe_router_loss_grad, moe_router_prepare,
-               moe_router_topk, lib)
+               moe_router_topk, lib, _chk)
 
 
 @dataclass
@@ -93,6 +93,7 @@ class MoELayer:
         # pooled counts of every rank instead of this rank's
         self.global_stats = None
         self.adapters = None  # set by enable_adapters(): low-rank adapters beside the router projection
+        self.graphs = self.graph_all = None  # set by capture()
 
     STAGES = ("router", "capacity", "dispatch", "ffn", "combine", "stats")
 
@@ -192,6 +193,8 @@ class MoELayer:
     def replay(self, events=None) -> torch.Tensor:
         """Replay the captured forward on the current stream: the whole-forward graph, or with
         `events` (7 CUDA events) the per-stage graphs with the events recorded between them."""
+        if self.graph_all is None:
+            raise RuntimeError("replay needs capture(), again after enable_adapters()")
         st = torch.cuda.current_stream()
         if events is None:
             self.graph_all.replay()
@@ -206,13 +209,22 @@ class MoELayer:
     def enable_adapters(self, a, b, scale, adapter_idx) -> None:
         """Give the router a low-rank adapter per token: from now on logits_i = x_i W_r + scale_q B_q (A_q x_i) with
         q = adapter_idx[i] (-1: none), for a [na, r, d] and b [na, n, r] of the layer's dtype, scale [na] fp32 and
-        adapter_idx [m] int32. The tensors are used in place: a captured forward follows their contents. The layer then
-        keeps what `router_backward` reads, among it the expert rows (ybuf), so one pick per token runs FFN and combine
-        apart."""
+        adapter_idx [m] int32. The tensors are used in place: a forward captured from now on follows their contents.
+        The call waits for the device and drops the layer's captured forward, which is another one: `replay` needs
+        `capture` again, and so does a graph that the caller made of this layer's calls. The layer then keeps what
+        `router_backward` reads, among it the expert rows (ybuf), so one pick per token runs FFN and combine apart."""
         s, dev = self.shape, self.device
-        na, r = a.shape[:2]
-        self.adapters = dict(a=a, b=b, scale=scale, adapter_idx=adapter_idx)
         f32, u8 = torch.float32, torch.uint8
+        if a.dim() != 3 or a.shape[2] != s.d:
+            raise ValueError(f"a: expected [n_adapters, rank, {s.d}], got {tuple(a.shape)}")
+        na, r = a.shape[:2]
+        on = self.buf["probs"].get_device()
+        for t, dtype, shape, name in ((a, s.dtype, (na, r, s.d), "a"), (b, s.dtype, (na, s.n, r), "b"),
+                                      (scale, f32, (na,), "scale"), (adapter_idx, torch.int32, (s.m,), "adapter_idx")):
+            _chk(on, t, dtype, shape, name)
+        torch.cuda.synchronize(dev)  # nothing still uses the graphs and buffers that go
+        self.graphs = self.graph_all = None
+        self.adapters = dict(a=a, b=b, scale=scale, adapter_idx=adapter_idx)
         self.buf["logits"] = torch.empty((s.m, s.n), dtype=f32, device=dev)
         self.buf["hidden"] = torch.empty((s.m, r), dtype=f32, device=dev)
         if self.ffn_combine:

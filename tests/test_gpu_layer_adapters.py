@@ -171,3 +171,28 @@ def test_router_backward_captured_before_a_larger_batch():
         assert t is None or torch.equal(got[key], t), key
     for key, t in keep.items():
         assert torch.equal(eager[key], t), key
+
+
+def test_capture_then_enable_then_enable_again():
+    layer, x, ad, dy = make("switch", r=8, **SWITCH)
+    _, _, other, _ = make("switch", seed=9, na=2, r=16, **SWITCH)
+    cuts = torch.tensor([0, 100, 512], dtype=torch.int32, device="cuda")
+    with pytest.raises(RuntimeError):
+        layer.replay()
+    layer.capture(x)
+    plain = layer.replay().clone()
+    for adapters in (ad, other, ad):
+        layer.enable_adapters(**adapters)
+        with pytest.raises(RuntimeError):
+            layer.replay()
+        layer.capture(x)
+        for t in layer.buf.values():  # what the replay does not write would show
+            if t.dtype.is_floating_point:
+                t.fill_(float("nan"))
+        got = layer.replay().clone()
+        out = layer.router_backward(x, dy, cuts)
+        lb.sync_status()
+        logits, hidden = lb.moe_router_adapters(x, layer.w["w_r"], **adapters)
+        assert torch.equal(layer.buf["logits"], logits) and torch.equal(layer.buf["hidden"], hidden)
+        assert not torch.equal(got, plain) and torch.equal(got, layer.forward(x))
+        assert all(bool(out[key].isfinite().all()) for key in ("da", "db", "dx", "dlogits"))

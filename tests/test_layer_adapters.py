@@ -24,8 +24,9 @@ def bare_layer(m=64, d=32, n=8, k=2, dtype=torch.bfloat16):
     layer.shape = L.LayerShape(m=m, d=d, n=n, k=k, d_ff=16, dtype=dtype)
     layer.device = torch.device("cpu")
     layer.w = dict(w_r=torch.zeros(d, n))
-    layer.buf = {key: torch.zeros(1) for key in ("ybuf", "dest_row", "topk_gate", "logits", "topk_idx", "hidden")}
-    layer.ws, layer.global_stats = {}, None
+    layer.buf = {key: torch.zeros(1) for key in ("ybuf", "dest_row", "topk_gate", "logits", "topk_idx", "hidden", "probs")}
+    layer.ws, layer.global_stats, layer.ffn_combine = {}, None, False
+    layer.graphs = layer.graph_all = None
     layer.adapters = dict(a=torch.zeros(3, 4, d), b=torch.zeros(3, n, 4), scale=torch.zeros(3),
                           adapter_idx=torch.zeros(m, dtype=torch.int32))
     return layer
@@ -41,3 +42,40 @@ def test_router_backward_leaves_workspaces_to_the_stream_of_each_call(calls):
                                            "moe_router_adapters_grad"] * 3
     assert all(kw["stream"] is side and kw.get("workspace") is None for _, kw in calls)
     assert not layer.ws
+
+
+def some_adapters(layer, na=3, r=4):
+    s = layer.shape
+    return dict(a=torch.zeros(na, r, s.d, dtype=s.dtype), b=torch.zeros(na, s.n, r, dtype=s.dtype), scale=torch.zeros(na),
+                adapter_idx=torch.zeros(s.m, dtype=torch.int32))
+
+
+def test_enable_adapters_drops_a_captured_forward(monkeypatch):
+    # a forward captured before is another one, and one captured with other adapters would write to buffers that are gone
+    waited = []
+    monkeypatch.setattr(torch.cuda, "synchronize", waited.append)
+    layer = bare_layer()
+
+    class Graph:
+        def replay(self):
+            raise AssertionError("a stale graph ran")
+    for _ in range(2):
+        layer.graphs, layer.graph_all = [Graph()] * 6, Graph()
+        layer.enable_adapters(**some_adapters(layer))
+        assert waited.pop() == layer.device
+        with pytest.raises(RuntimeError, match="capture"):
+            layer.replay()
+
+
+@pytest.mark.parametrize("key,bad", [
+    ("a", torch.zeros(3, 4, 24, dtype=torch.bfloat16)), ("a", torch.zeros(3, 4, 32)), ("a", torch.zeros(4, 32, dtype=torch.bfloat16)),
+    ("b", torch.zeros(3, 4, 8, dtype=torch.bfloat16)), ("b", torch.zeros(2, 8, 4, dtype=torch.bfloat16)), ("scale", torch.zeros(2)),
+    ("adapter_idx", torch.zeros(63, dtype=torch.int32)), ("adapter_idx", torch.zeros(64, dtype=torch.int64))])
+def test_enable_adapters_refuses_and_changes_nothing(monkeypatch, key, bad):
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda dev: None)
+    layer = bare_layer()
+    before, buf = layer.adapters, dict(layer.buf)
+    layer.graphs = layer.graph_all = "captured"
+    with pytest.raises(ValueError, match=key):
+        layer.enable_adapters(**dict(some_adapters(layer), **{key: bad}))
+    assert layer.adapters is before and layer.buf == buf and layer.graph_all == "captured"
