@@ -105,6 +105,7 @@ class MoELayer:
             if ad is not None:
                 moe_router_adapters(x, w["w_r"], ad["a"], ad["b"], ad["adapter_idx"], ad["scale"], logits=b["logits"],
                                     hidden=b["hidden"], workspace=self.ws["adapters"], stream=st)
+                ad["ran"] = True
                 moe_router_topk(None, None, s.n, s.k, fn, s.renorm_topk, rank_bias=w.get("rank_bias"),
                                 logits_in=b["logits"], probs_out=b["probs"], topk_idx=b["topk_idx"],
                                 topk_gate=b["topk_gate"], stream=st)
@@ -224,7 +225,7 @@ class MoELayer:
             _chk(on, t, dtype, shape, name)
         torch.cuda.synchronize(dev)  # nothing still uses the graphs and buffers that go
         self.graphs = self.graph_all = None
-        self.adapters = dict(a=a, b=b, scale=scale, adapter_idx=adapter_idx)
+        self.adapters = dict(a=a, b=b, scale=scale, adapter_idx=adapter_idx, ran=False)
         self.buf["logits"] = torch.empty((s.m, s.n), dtype=f32, device=dev)
         self.buf["hidden"] = torch.empty((s.m, r), dtype=f32, device=dev)
         if self.ffn_combine:
@@ -239,7 +240,7 @@ class MoELayer:
         router's own losses over the ragged sequences (`moe_router_loss` with this layer's alpha) to the gradients of
         the adapters. Returns dict(da, db, dw_r or None, dx or None (through the router alone), dybuf (of the expert
         rows, for the experts' backward), dgate, dlogits and moe_router_loss's loss, counts, tokens, f, P)."""
-        if self.adapters is None:
+        if self.adapters is None or not self.adapters["ran"]:
             raise RuntimeError("router_backward needs enable_adapters() and a forward")
         s, b, w, ad = self.shape, self.buf, self.w, self.adapters
         fn = MOE_SOFTMAX if s.score_fn == "softmax" else MOE_SIGMOID

@@ -28,7 +28,7 @@ def bare_layer(m=64, d=32, n=8, k=2, dtype=torch.bfloat16):
     layer.ws, layer.global_stats, layer.ffn_combine = {}, None, False
     layer.graphs = layer.graph_all = None
     layer.adapters = dict(a=torch.zeros(3, 4, d), b=torch.zeros(3, n, 4), scale=torch.zeros(3),
-                          adapter_idx=torch.zeros(m, dtype=torch.int32))
+                          adapter_idx=torch.zeros(m, dtype=torch.int32), ran=True)
     return layer
 
 
@@ -79,3 +79,20 @@ def test_enable_adapters_refuses_and_changes_nothing(monkeypatch, key, bad):
     with pytest.raises(ValueError, match=key):
         layer.enable_adapters(**dict(some_adapters(layer), **{key: bad}))
     assert layer.adapters is before and layer.buf == buf and layer.graph_all == "captured"
+
+
+def test_router_backward_needs_a_forward_with_these_adapters(monkeypatch, calls):
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda dev: None)
+    layer = bare_layer()
+    args = torch.zeros(64, 32), torch.zeros(64, 32), torch.zeros(2, dtype=torch.int32)
+    layer.router_backward(*args)
+    layer.enable_adapters(**some_adapters(layer))
+    del calls[:]
+    with pytest.raises(RuntimeError, match="forward"):  # logits and hidden are not there yet
+        layer.router_backward(*args)
+    assert not calls
+    monkeypatch.setattr(L, "moe_router_adapters", lambda *a, **kw: None)
+    monkeypatch.setattr(L, "moe_router_topk", lambda *a, **kw: None)
+    layer._stage(0, args[0], None)
+    layer.router_backward(*args)
+    assert len(calls) == 4
