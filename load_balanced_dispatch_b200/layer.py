@@ -239,9 +239,14 @@ class MoELayer:
         """The backward of the router after a forward with adapters (enable_adapters): from dy = dL/dy and the
         router's own losses over the ragged sequences (`moe_router_loss` with this layer's alpha) to the gradients of
         the adapters. Returns dict(da, db, dw_r or None, dx or None (through the router alone), dybuf (of the expert
-        rows, for the experts' backward), dgate, dlogits and moe_router_loss's loss, counts, tokens, f, P)."""
+        rows, for the experts' backward), dgate, dlogits and moe_router_loss's loss, counts, tokens, f, P). The balance
+        loss is that of this rank's sequences, so a layer that pools its statistics (enable_global_stats) is refused:
+        moe_router_loss_grad gives the pooled loss's gradient when the last rows of counts and tokens are the ranks' sums
+        (alpha_seq 0)."""
         if self.adapters is None or not self.adapters["ran"]:
             raise RuntimeError("router_backward needs enable_adapters() and a forward")
+        if self.global_stats is not None:
+            raise RuntimeError("router_backward has this rank's balance loss, not the pooled one of enable_global_stats()")
         s, b, w, ad = self.shape, self.buf, self.w, self.adapters
         fn = MOE_SOFTMAX if s.score_fn == "softmax" else MOE_SIGMOID
         coef = dict(token_mask=token_mask, score_fn=fn, alpha=s.alpha, alpha_seq=alpha_seq, z_coef=z_coef, stream=stream)

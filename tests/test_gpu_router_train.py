@@ -746,3 +746,27 @@ def test_gate_gradient_by_differences_of_the_router(fn, renorm, k):
     bound = 16 * EPS * mag / step + 48 * 8 * step ** 2 / 6 * mag + 64 * EPS * (dh.abs() * v.abs()).sum(1) + 1e-9
     assert bool(((diff - (dh.double() * v).sum(1)).abs() <= bound).all())
     assert fn == 1 or renorm == 0 or k > 1 or bool((dh.abs().sum(1) > 0).any())
+
+
+@pytest.mark.parametrize("fn", [0, 1])
+def test_router_loss_gradient_with_pooled_counts(fn):
+    # two ranks that put the sums of both into the last rows get the gradient of the loss of both batches
+    h, idx, _, tm, _ = loss_inputs(700, 48, 2, 3, True, 33)
+    cut, coef = 300, dict(alpha=1e-2, z_coef=1e-3)
+    whole = torch.tensor([0, 700], dtype=torch.int32, device="cuda")
+    both = lb.moe_router_loss(h, idx, whole, tm, fn, **coef)
+    want = lb.moe_router_loss_grad(h, idx, whole, both["counts"], both["tokens"], tm, fn, **coef)
+    parts = []
+    for rows in (slice(0, cut), slice(cut, 700)):
+        part = [t[rows].contiguous() for t in (h, idx, tm)]
+        ends = torch.tensor([0, len(part[0])], dtype=torch.int32, device="cuda")
+        parts.append((part, ends, lb.moe_router_loss(part[0], part[1], ends, part[2], fn, **coef)))
+    counts = sum(out["counts"][-1] for _, _, out in parts)
+    tokens = sum(out["tokens"][-1] for _, _, out in parts)
+    assert torch.equal(counts, both["counts"][-1]) and int(tokens) == int(both["tokens"][-1])
+    got = []
+    for (ph, pi, pm), ends, out in parts:
+        out["counts"][-1], out["tokens"][-1] = counts, tokens
+        got.append(lb.moe_router_loss_grad(ph, pi, ends, out["counts"], out["tokens"], pm, fn, **coef))
+    lb.sync_status()
+    assert torch.equal(torch.cat(got), want)

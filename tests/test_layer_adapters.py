@@ -96,3 +96,12 @@ def test_router_backward_needs_a_forward_with_these_adapters(monkeypatch, calls)
     layer._stage(0, args[0], None)
     layer.router_backward(*args)
     assert len(calls) == 4
+
+
+def test_router_backward_refuses_pooled_statistics(calls):
+    # the layer's balance loss is then the pooled one, whose gradient does not follow from this rank's counts
+    layer = bare_layer()
+    layer.global_stats = dict(m_total=128)
+    with pytest.raises(RuntimeError, match="pooled"):
+        layer.router_backward(torch.zeros(64, 32), torch.zeros(64, 32), torch.zeros(2, dtype=torch.int32))
+    assert not calls
