@@ -104,7 +104,7 @@ class MoELayer:
             ad = self.adapters
             if ad is not None:
                 moe_router_adapters(x, w["w_r"], ad["a"], ad["b"], ad["adapter_idx"], ad["scale"], logits=b["logits"],
-                                    hidden=b["hidden"], workspace=self.ws["adapters"], stream=st)
+                                    hidden=b.get("hidden"), want_hidden=ad["backward"], workspace=self.ws["adapters"], stream=st)
                 ad["ran"] = True
                 moe_router_topk(None, None, s.n, s.k, fn, s.renorm_topk, rank_bias=w.get("rank_bias"),
                                 logits_in=b["logits"], probs_out=b["probs"], topk_idx=b["topk_idx"],
@@ -207,13 +207,14 @@ class MoELayer:
         events[len(self.graphs)].record(st)
         return self.buf["y"]
 
-    def enable_adapters(self, a, b, scale, adapter_idx) -> None:
+    def enable_adapters(self, a, b, scale, adapter_idx, backward=True) -> None:
         """Give the router a low-rank adapter per token: from now on logits_i = x_i W_r + scale_q B_q (A_q x_i) with
         q = adapter_idx[i] (-1: none), for a [na, r, d] and b [na, n, r] of the layer's dtype, scale [na] fp32 and
         adapter_idx [m] int32. The tensors are used in place: a forward captured from now on follows their contents.
         The call waits for the device and drops the layer's captured forward, which is another one: `replay` needs
-        `capture` again, and so does a graph that the caller made of this layer's calls. The layer then keeps what
-        `router_backward` reads, among it the expert rows (ybuf), so one pick per token runs FFN and combine apart."""
+        `capture` again, and so does a graph that the caller made of this layer's calls. With `backward` the layer keeps
+        what `router_backward` reads, among it the expert rows (ybuf), so one pick per token runs FFN and combine apart;
+        without it (serving) the forward stays as it was behind the router."""
         s, dev = self.shape, self.device
         f32, u8 = torch.float32, torch.uint8
         if a.dim() != 3 or a.shape[2] != s.d:
@@ -223,16 +224,29 @@ class MoELayer:
         for t, dtype, shape, name in ((a, s.dtype, (na, r, s.d), "a"), (b, s.dtype, (na, s.n, r), "b"),
                                       (scale, f32, (na,), "scale"), (adapter_idx, torch.int32, (s.m,), "adapter_idx")):
             _chk(on, t, dtype, shape, name)
-        torch.cuda.synchronize(dev)  # nothing still uses the graphs and buffers that go
-        self.graphs = self.graph_all = None
-        self.adapters = dict(a=a, b=b, scale=scale, adapter_idx=adapter_idx, ran=False)
+        self.disable_adapters()
+        self.adapters = dict(a=a, b=b, scale=scale, adapter_idx=adapter_idx, backward=backward, ran=False,
+                             split_combine=backward and self.ffn_combine)
         self.buf["logits"] = torch.empty((s.m, s.n), dtype=f32, device=dev)
-        self.buf["hidden"] = torch.empty((s.m, r), dtype=f32, device=dev)
-        if self.ffn_combine:
+        if backward:
+            self.buf["hidden"] = torch.empty((s.m, r), dtype=f32, device=dev)
+        if self.adapters["split_combine"]:
             self.ffn_combine = False
             self.buf["ybuf"] = torch.empty((self.rows_max, s.d), dtype=s.dtype, device=dev)
         size = moe_router_adapters_workspace_size(s.m, s.d, s.n, r, na, s.dtype)
         self.ws["adapters"] = torch.empty((max(size, 1),), dtype=u8, device=dev)
+
+    def disable_adapters(self) -> None:
+        """Back to the layer without adapters. As enable_adapters, it waits for the device and drops the captured
+        forward."""
+        torch.cuda.synchronize(self.device)  # nothing still uses the graphs and buffers that go
+        self.graphs = self.graph_all = None
+        if self.adapters is not None and self.adapters["split_combine"]:
+            self.ffn_combine = True
+            self.buf["ybuf"] = torch.empty((0, self.shape.d), dtype=self.shape.dtype, device=self.device)
+        self.adapters = None
+        for store, key in ((self.buf, "logits"), (self.buf, "hidden"), (self.ws, "adapters")):
+            store.pop(key, None)
 
     def router_backward(self, x, dy, seq_offsets, token_mask=None, alpha_seq=0.0, z_coef=0.0, dloss=None,
                         want_dx=True, want_dw_r=False, stream=None) -> dict:
@@ -243,8 +257,8 @@ class MoELayer:
         loss is that of this rank's sequences, so a layer that pools its statistics (enable_global_stats) is refused:
         moe_router_loss_grad gives the pooled loss's gradient when the last rows of counts and tokens are the ranks' sums
         (alpha_seq 0)."""
-        if self.adapters is None or not self.adapters["ran"]:
-            raise RuntimeError("router_backward needs enable_adapters() and a forward")
+        if self.adapters is None or not self.adapters["backward"] or not self.adapters["ran"]:
+            raise RuntimeError("router_backward needs enable_adapters(backward=True) and a forward")
         if self.global_stats is not None:
             raise RuntimeError("router_backward has this rank's balance loss, not the pooled one of enable_global_stats()")
         s, b, w, ad = self.shape, self.buf, self.w, self.adapters

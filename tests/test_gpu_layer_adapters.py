@@ -196,3 +196,24 @@ def test_capture_then_enable_then_enable_again():
         assert torch.equal(layer.buf["logits"], logits) and torch.equal(layer.buf["hidden"], hidden)
         assert not torch.equal(got, plain) and torch.equal(got, layer.forward(x))
         assert all(bool(out[key].isfinite().all()) for key in ("da", "db", "dx", "dlogits"))
+
+
+@pytest.mark.parametrize("name,kw,r", [("tiny", TINY, 4), ("global", GLOBAL, 16), ("switch", SWITCH, 8)])
+def test_serving_forward_and_back_to_the_plain_layer(name, kw, r):
+    layer, x, ad, _ = make(name, r=r, **kw)
+    fused, launches = layer.ffn_combine, layer.launches_per_forward()
+    plain = layer.forward(x).clone()
+    layer.enable_adapters(**ad)
+    want = layer.forward(x).clone()
+    layer.enable_adapters(**ad, backward=False)
+    assert layer.ffn_combine == fused == (layer.buf["ybuf"].shape[0] == 0)
+    assert torch.equal(layer.forward(x), want)
+    layer.capture(x)
+    assert torch.equal(layer.replay(), want)
+    layer.disable_adapters()
+    with pytest.raises(RuntimeError):
+        layer.replay()
+    assert torch.equal(layer.forward(x), plain) and layer.launches_per_forward() == launches
+    layer.capture(x)
+    assert torch.equal(layer.replay(), plain)
+    lb.sync_status()

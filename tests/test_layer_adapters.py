@@ -28,7 +28,8 @@ def bare_layer(m=64, d=32, n=8, k=2, dtype=torch.bfloat16):
     layer.ws, layer.global_stats, layer.ffn_combine = {}, None, False
     layer.graphs = layer.graph_all = None
     layer.adapters = dict(a=torch.zeros(3, 4, d), b=torch.zeros(3, n, 4), scale=torch.zeros(3),
-                          adapter_idx=torch.zeros(m, dtype=torch.int32), ran=True)
+                          adapter_idx=torch.zeros(m, dtype=torch.int32), backward=True, ran=True,
+                          split_combine=False)
     return layer
 
 
@@ -105,3 +106,28 @@ def test_router_backward_refuses_pooled_statistics(calls):
     with pytest.raises(RuntimeError, match="pooled"):
         layer.router_backward(torch.zeros(64, 32), torch.zeros(64, 32), torch.zeros(2, dtype=torch.int32))
     assert not calls
+
+
+def test_serving_keeps_the_fused_combine_and_refuses_the_backward(monkeypatch, calls):
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda dev: None)
+    layer = bare_layer(k=1)
+    layer.disable_adapters()
+    layer.ffn_combine, layer.rows_max = True, 64
+    layer.buf["ybuf"] = torch.zeros(0, 32, dtype=torch.bfloat16)
+    args = torch.zeros(64, 32), torch.zeros(64, 32), torch.zeros(2, dtype=torch.int32)
+    for backward in (False, True, True, False):
+        layer.enable_adapters(**some_adapters(layer), backward=backward)
+        assert layer.ffn_combine is not backward
+        assert layer.buf["ybuf"].shape == ((64 if backward else 0), 32) and ("hidden" in layer.buf) == backward
+        layer.adapters["ran"] = True
+        if backward:
+            layer.router_backward(*args)
+        else:
+            with pytest.raises(RuntimeError, match="backward"):
+                layer.router_backward(*args)
+    layer.enable_adapters(**some_adapters(layer))
+    layer.disable_adapters()
+    assert layer.adapters is None and layer.ffn_combine and layer.buf["ybuf"].shape == (0, 32)
+    assert not {"logits", "hidden"} & set(layer.buf) and "adapters" not in layer.ws
+    with pytest.raises(RuntimeError):
+        layer.router_backward(*args)
