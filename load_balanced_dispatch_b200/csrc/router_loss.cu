@@ -17,7 +17,10 @@
 //   router_loss_grad_kernel   one pass: logits in, gradient out.
 //
 // No floating-point atomics, every fold in a fixed order: the results are bit-reproducible.
-// Bound by reading the logits (and writing the gradient): 4 m n bytes each.
+// Reading the logits (and writing the gradient) is 4 m n bytes each; both passes wait for instruction issue before
+// that (65536 x 256, k 8: 36 and 54 us). The exponentials are expf, as the router's are: __expf is off by 1.2 |x| ulp,
+// which is many in the scores of experts far below a row's best, and with scores added in fp32 by twos and fours
+// before the fp64 sums it saved 3 and 5 of these microseconds.
 #include "common.cuh"
 
 namespace moe {
@@ -112,8 +115,6 @@ __device__ __forceinline__ float lanes_max(float v) {
     return v;
 }
 
-// The exponentials are __expf (off by 2 + 1.2 |x| ulp, which is below 2^-18 where exp(x) is above 2^-24 of a row's
-// sum); expf made the passes wait for instruction issue, at 37 and 56 instructions a logit.
 // h_j <- exp(h_j - top) / sum, and the log-sum-exp of a row held by L lanes. A row whose logits are
 // all -inf has no scores: 0 throughout and lse = 0. NaN and +inf give NaN.
 template <int L, int V>
@@ -125,7 +126,7 @@ __device__ __forceinline__ float row_softmax(float (&h)[4 * V]) {
     if (top == -INFINITY) top = 0.f;
     float s = 0.f;
 #pragma unroll
-    for (int q = 0; q < 4 * V; ++q) { h[q] = __expf(h[q] - top); s += h[q]; }
+    for (int q = 0; q < 4 * V; ++q) { h[q] = expf(h[q] - top); s += h[q]; }
     s = lanes_sum<L>(s);
     const float inv = s == 0.f ? 0.f : 1.f / s;
 #pragma unroll
@@ -133,7 +134,7 @@ __device__ __forceinline__ float row_softmax(float (&h)[4 * V]) {
     return s == 0.f ? 0.f : top + logf(s);
 }
 
-__device__ __forceinline__ float logistic(float h) { return __fdividef(1.f, 1.f + __expf(-h)); }
+__device__ __forceinline__ float logistic(float h) { return 1.f / (1.f + expf(-h)); }
 
 template <int L, int V>
 __global__ void __launch_bounds__(rloss::kThreads, 4)
@@ -217,14 +218,10 @@ router_loss_chunk_kernel(const float* __restrict__ logits, const int32_t* __rest
                     }
                 }
             }
-            // U scores are added in fp32, the sums over the rounds in fp64
 #pragma unroll
-            for (int q = 0; q < 4 * V; ++q) {
-                float t = h[0][q];
-                if constexpr (U == 2) t = h[0][q] + h[1][q];
-                if constexpr (U == 4) t = (h[0][q] + h[1][q]) + (h[2][q] + h[3][q]);
-                acc[q] += (double)t;
-            }
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int q = 0; q < 4 * V; ++q) acc[q] += (double)h[u][q];
         }
         // column 4 (sub + L v) + q of row group g sits at fold[g][4 (sub + L v) + q]
 #pragma unroll
@@ -509,21 +506,23 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
         for (int u = 0; u < U; ++u) {
             s[u] = eg[u] = 0.f;
             if (top[u] == -INFINITY) top[u] = 0.f;  // a row without scores
+            if (soft || cz != 0.f) {
 #pragma unroll
-            for (int q = 0; q < 4 * V; ++q) {
-                e[u][q] = __expf(h[u][q] - top[u]);
-                s[u] += e[u][q];
-                eg[u] = fmaf(e[u][q], g[u][q], eg[u]);
+                for (int q = 0; q < 4 * V; ++q) {
+                    e[u][q] = expf(h[u][q] - top[u]);
+                    s[u] += e[u][q];
+                    eg[u] = fmaf(e[u][q], g[u][q], eg[u]);
+                }
             }
             if (ptop[u] == -INFINITY) ptop[u] = 0.f;  // no pick has a score: every weight is 0
-            w0[u] = chosen ? __expf(x0[u] - ptop[u]) : 0.f;
+            w0[u] = chosen ? expf(x0[u] - ptop[u]) : 0.f;
             sq[u] = w0[u];
             dq[u] = w0[u] * dg[u];
             if (chosen)
                 for (int t = sub + L; t < k; t += L) {
                     const int p = live[u] ? idx[(r0 + i + u) * k + t] : -1;
                     if (p >= 0 && p < n) {
-                        const float x = __expf(mine[u * 2 * CW + p] - ptop[u]);
+                        const float x = expf(mine[u * 2 * CW + p] - ptop[u]);
                         sq[u] += x;
                         dq[u] = fmaf(x, dgate[(r0 + i + u) * k + t], dq[u]);
                     }
@@ -550,9 +549,10 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
                 for (int q = 0; q < 4 * V; ++q) e[u][q] *= inv * (g[u][q] - c);
             } else {
 #pragma unroll
-                for (int q = 0; q < 4 * V; ++q) {  // 1 - rho from its own exponential: exact for large h
+                for (int q = 0; q < 4 * V; ++q) {  // rho (1 - rho) = t / (1 + t)^2, t = exp(-|h|): exact for large h
                     const float z = cz != 0.f ? cz * lse * inv * e[u][q] : 0.f;
-                    e[u][q] = fmaf(g[u][q] * logistic(h[u][q]), logistic(-h[u][q]), z);
+                    const float t = expf(-fabsf(h[u][q])), w = 1.f / (1.f + t);
+                    e[u][q] = fmaf(g[u][q] * w, t * w, z);
                 }
             }
             if (chosen) {  // dL/dh of a pick: q_r (dg_r - sum q dg)
@@ -562,7 +562,7 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
                 for (int t = sub + L; t < k; t += L) {
                     const int p = live[u] ? idx[(r0 + i + u) * k + t] : -1;
                     if (p >= 0 && p < n)
-                        atomicAdd(&add[p], __expf(mine[u * 2 * CW + p] - ptop[u]) * iq * (dgate[(r0 + i + u) * k + t] - dot));
+                        atomicAdd(&add[p], expf(mine[u * 2 * CW + p] - ptop[u]) * iq * (dgate[(r0 + i + u) * k + t] - dot));
                 }
             }
         }

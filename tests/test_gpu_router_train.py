@@ -770,3 +770,26 @@ def test_router_loss_gradient_with_pooled_counts(fn):
         got.append(lb.moe_router_loss_grad(ph, pi, ends, out["counts"], out["tokens"], pm, fn, **coef))
     lb.sync_status()
     assert torch.equal(torch.cat(got), want)
+
+
+@pytest.mark.parametrize("fn", [0, 1])
+@pytest.mark.parametrize("n", [8, 16, 32, 64, 100, 200])
+def test_router_loss_scores_are_right_to_a_few_roundings(fn, n):
+    # logits that are multiples of 2^-5 down to -84: differences from the row's best are exact, so a score is off by the
+    # exponential (2 ulp, four times 2^-24), the sum (that and 16 additions), the quotient and the product alone,
+    # 2^-24 * (4 + 4 + 16 + 2); the mean is taken in 64 bits and rounded once. A logistic: 4 and two roundings
+    m, k = 300, 2
+    g = gen(81)
+    step = torch.floor(torch.tensor(84.0 * 32 / (n - 1))) / 32
+    h = (-step * torch.arange(n)).float().cuda()[torch.stack([torch.randperm(n, generator=g, device="cuda") for _ in range(m)])]
+    h[:100] = h[0]
+    h = h.contiguous()
+    idx = torch.topk(h, k, dim=1).indices.to(torch.int32).contiguous()
+    cuts = torch.tensor([0, 100, m], dtype=torch.int32, device="cuda")
+    ref = loss_ref(h, idx, cuts, None, fn, 1e-2, 0.0, 0.0)
+    out = lb.moe_router_loss(h, idx, cuts, None, fn)
+    dh = lb.moe_router_loss_grad(h, idx, cuts, out["counts"], out["tokens"], None, fn)
+    lb.sync_status()
+    within(out["P"], ref["P"], (27 if fn == 0 else 8) * 2.0 ** -24 * ref["P"], "P")
+    # softmax, p (g - sum p g): g 3 roundings, p 26, the sum 26 and 3 and 16; logistic, g t w w: 3, 4, 6, 6 and 3
+    within(dh, ref["dlogits"], (80 if fn == 0 else 24) * 2.0 ** -24 * ref["mag"] + 1e-37, "dlogits")
