@@ -793,3 +793,49 @@ def test_router_loss_scores_are_right_to_a_few_roundings(fn, n):
     within(out["P"], ref["P"], (27 if fn == 0 else 8) * 2.0 ** -24 * ref["P"], "P")
     # softmax, p (g - sum p g): g 3 roundings, p 26, the sum 26 and 3 and 16; logistic, g t w w: 3, 4, 6, 6 and 3
     within(dh, ref["dlogits"], (80 if fn == 0 else 24) * 2.0 ** -24 * ref["mag"] + 1e-37, "dlogits")
+
+
+@pytest.mark.parametrize("order", ["runs", "mixed"])
+@pytest.mark.parametrize("m,d,n,r,na", [
+    (2600, 512, 64, 16, 6),    # W_r's parts and A_a in one operand
+    (2600, 200, 128, 40, 3),   # two column tiles, rank above 32
+    (20000, 64, 128, 8, 5),    # operands apart: 128 and 96 columns
+    (19500, 72, 90, 32, 3), (2300, 136, 200, 64, 2)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_adapters_do_not_mix_rows_on_the_tensor_cores(m, d, n, r, na, order, bad):
+    # the rows before and behind a group's end: a box of 32 rows takes in rows of the next group, stages keep old rows
+    i, dh = adapter_inputs(m, d, n, r, na, torch.bfloat16, order, m + n)
+    assert lb.moe_router_adapters_workspace_size(m, d, n, r, na) > 0  # not the kernel of few rows
+    idx = i["adapter_idx"]
+    ends = (idx[1:] != idx[:-1]).nonzero()[:, 0]
+    ends = ends[torch.randperm(len(ends), generator=gen(5), device="cuda")[:7]]
+    clean = lb.moe_router_adapters(**i)
+    want = lb.moe_router_adapters_grad(dh, hidden=clean[1], want_dw_r=True, **i)
+    for rows in (ends, ends + 1, torch.tensor([0, m - 1], device="cuda")):
+        rest = torch.ones(m, dtype=torch.bool, device="cuda")
+        rest[rows] = False
+        x = i["x"].clone()
+        x[rows, 3] = bad
+        logits, hidden = lb.moe_router_adapters(**dict(i, x=x))
+        assert torch.equal(logits[rest], clean[0][rest]) and torch.equal(hidden[rest], clean[1][rest])
+        assert not bool(logits[rows].isfinite().any())
+        assert not bool(hidden[rows][idx[rows] >= 0].isfinite().any()) and not bool(hidden[rows][idx[rows] < 0].any())
+        hit = torch.zeros(na, dtype=torch.bool, device="cuda")
+        hit[idx[rows][idx[rows] >= 0].long()] = True
+        cols = torch.arange(d, device="cuda") != 3
+        # x: column 3 of its adapters' dA and of dW_r, nothing else
+        dx, da, db, dw = lb.moe_router_adapters_grad(dh, hidden=clean[1], want_dw_r=True, **dict(i, x=x))
+        assert torch.equal(dx, want[0]) and torch.equal(db, want[2])
+        assert torch.equal(da[~hit], want[1][~hit]) and torch.equal(da[:, :, cols], want[1][:, :, cols])
+        assert not bool(da[hit][:, :, 3].isfinite().any())
+        assert torch.equal(dw[cols], want[3][cols]) and not bool(dw[3].isfinite().any())
+        # dlogits: its own row of dx, its adapters' dA and dB, a column of dW_r
+        dh2 = dh.clone()
+        dh2[rows, 1] = bad
+        dx, da, db, dw = lb.moe_router_adapters_grad(dh2, hidden=clean[1], want_dw_r=True, **i)
+        assert torch.equal(dx[rest], want[0][rest]) and not bool(dx[rows].isfinite().any())
+        assert torch.equal(da[~hit], want[1][~hit]) and torch.equal(db[~hit], want[2][~hit])
+        assert not bool(da[hit].isfinite().any()) and not bool(db[hit][:, 1].isfinite().any())
+        other = torch.arange(n, device="cuda") != 1
+        assert torch.equal(dw[:, other], want[3][:, other]) and not bool(dw[:, 1].isfinite().any())
+    lb.sync_status()
