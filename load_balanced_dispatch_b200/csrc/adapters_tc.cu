@@ -172,7 +172,7 @@ router_adapters_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __gri
                     __syncwarp();
                     if (warp == 0) {
                         // B rows: fused [W0 W1 W2 A], else [W0 A W1 W2]
-if (lane >= 8 && lane < 11) {
+                        if (lane >= 8 && lane < 11) {
                             const int p = lane - 8;
                             const int row = p * NP + (!T::FUSED && p > 0 ? RP : 0);
                             ptx::tma_load_3d(sb + row * 128, &map_w, bar, kb * BK, ct * NP, p);
@@ -341,7 +341,8 @@ if (lane >= 8 && lane < 11) {
             }
             if (finish && ad) {  // the same for all eight warps
                 // s B_a u by the tensor core: s u in three bf16 parts that add up to it, in tensor memory, and B_a
-                // (exact) in shared memory; a few hundred instructions, against 30 to 80 KB of unrolled products
+                // (exact) in shared memory. Against products by FMA: 41 for 54 us (8191 rows of 768, n 128, rank 8), 148
+                // for 155 us (65536 rows of 4096, n 64, rank 16)
                 if (ok) {
                     const float s = scale[g];
                     const uint32_t ut = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(T::UCOL + half * T::USTEP);
