@@ -18,9 +18,9 @@
 //
 // No floating-point atomics, every fold in a fixed order: the results are bit-reproducible.
 // Reading the logits (and writing the gradient) is 4 m n bytes each; both passes wait for instruction issue before
-// that (65536 x 256, k 8: 36 and 54 us). The exponentials are expf, as the router's are: __expf is off by 1.2 |x| ulp,
+// that (65536 x 256, k 8: 36 and 53 us). The exponentials are expf, as the router's are: __expf is off by 1.2 |x| ulp,
 // which is many in the scores of experts far below a row's best, and with scores added in fp32 by twos and fours
-// before the fp64 sums it saved 3 and 5 of these microseconds.
+// before the fp64 sums it saved 3 and 4 of these microseconds.
 #include "common.cuh"
 
 namespace moe {
@@ -391,21 +391,25 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
     const float cz = (float)(2.0 * z_coef * up / T);
     const bool chosen = soft && renorm && k > 1 && dgate;  // gate = softmax over the picks
     const double full = alpha_seq != 0.0 ? (double)max(s_full, 1) : 1.0;
-    // a table row's part of g for the owned columns: coef / T * (count n - k T) / (k T), or coef / T * count n / (k T)
-    auto table = [&](const int32_t* row, int64_t t, double coef, float (&g)[4 * V]) {
-        const float scale = (float)(coef / ((double)t * (double)t * (double)k));
+    // g for the owned columns, rounded once: a table row's part is coef / T * (count n - k T) / (k T), without the k T
+    // above for a logistic; the whole batch's row and (s < nseq) sequence s's
+    float gt[4 * V];
+    auto table = [&](int s) {
+        const int t = s < nseq ? max(tokens[s], 1) : 1;
+        const double cG = up * alpha / ((double)T * T * k), cs = s < nseq ? up * alpha_seq / (full * t * t * k) : 0.0;
+        const double zG = soft ? (double)k * T : 0.0, zs = soft ? (double)k * t : 0.0;
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int j = 4 * (sub + L * v) + q;
-                g[4 * v + q] = j < n ? scale * (float)((int64_t)row[j] * n - (soft ? (int64_t)k * t : 0)) : 0.f;
+                double g = 0.0;
+                if (j < n) g = cG * ((double)counts[(int64_t)nseq * n + j] * n - zG);
+                if (j < n && s < nseq) g += cs * ((double)counts[(int64_t)s * n + j] * n - zs);
+                gt[4 * v + q] = (float)g;
             }
     };
-    float gG[4 * V], gt[4 * V];  // the whole batch's part; with the row's sequence
-    table(counts + (int64_t)nseq * n, T, up * alpha, gG);
-#pragma unroll
-    for (int q = 0; q < 4 * V; ++q) gt[q] = gG[q];
+    table(nseq);
     const int64_t groups = (int64_t)gridDim.x * GROUPS, per = (m + groups - 1) / groups;
     const int64_t r0 = ((int64_t)blockIdx.x * GROUPS + grp) * per, r1 = min(r0 + per, m);
     int seq = -2;
@@ -437,11 +441,7 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
             if (i + u < per && r < r1 && r >= seq_end) {
                 seq = seq_of_row(off, nseq, r);
                 seq_end = seq >= nseq ? m : (int64_t)off[seq + 1];
-                if (alpha_seq != 0.0 && seq >= 0 && seq < nseq) {
-                    table(counts + (int64_t)seq * n, max(tokens[seq], 1), up * alpha_seq / full, gt);
-#pragma unroll
-                    for (int q = 0; q < 4 * V; ++q) gt[q] += gG[q];
-                }
+                if (alpha_seq != 0.0 && seq >= 0 && seq < nseq) table(seq);
             }
             live[u] = live[u] && seq >= 0 && seq < nseq;
             if (!live[u] || pick[u] < 0 || pick[u] >= n) pick[u] = -1;
@@ -551,8 +551,8 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
 #pragma unroll
                 for (int q = 0; q < 4 * V; ++q) {  // rho (1 - rho) = t / (1 + t)^2, t = exp(-|h|): exact for large h
                     const float z = cz != 0.f ? cz * lse * inv * e[u][q] : 0.f;
-                    const float t = expf(-fabsf(h[u][q])), w = 1.f / (1.f + t);
-                    e[u][q] = fmaf(g[u][q] * w, t * w, z);
+                    const float t = expf(-fabsf(h[u][q])), s1 = 1.f + t, lost = t - (s1 - 1.f);  // 1 + t = s1 + lost
+                    e[u][q] = fmaf(g[u][q], t / fmaf(s1, s1, 2.f * s1 * lost), z);
                 }
             }
             if (chosen) {  // dL/dh of a pick: q_r (dg_r - sum q dg)
