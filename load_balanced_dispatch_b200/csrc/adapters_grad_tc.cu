@@ -16,7 +16,7 @@
 // three bf16 parts, is scaled alike and added to the same sums; the drain takes the powers out again. Two bf16 parts a
 // side without scales have 16 bits, which shows in dx where W_r's rows have much in common (the gradient of a
 // softmax adds up to zero, so that cancels). dx of 65536 rows, d 4096, n 64, rank 16: 131 us with two bf16 parts,
-// 143 us so, 205 us with three bf16 parts and six products.
+// 142 us so, 205 us with three bf16 parts and six products.
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -230,8 +230,9 @@ adapters_split_kernel(const float* __restrict__ dh, const float* __restrict__ hi
                 }
             };
             const int64_t at = (int64_t)(p0 + q) * PC + part * JT;
-            store(out.dup + at, 1.f);
-            if (out.dus && part * JT < (r + 15) / 16 * 16) store(out.dus + at, srow[q]);  // dx stops at whole 16 ranks
+            // ranks behind r: dA's are not stored, dx's are multiplied up to whole 16
+            if (part * JT < r) store(out.dup + at, 1.f);
+            if (out.dus && part * JT < (r + 15) / 16 * 16) store(out.dus + at, srow[q]);
         }
         float part[NE][NJ];
 #pragma unroll
@@ -317,6 +318,7 @@ struct AdxTile {
     static_assert(ND / 64 * RP * 128 <= SLOT && SLOT >= 16384, "A_a and a chunk of du fit a slot");
 };
 
+// The drain's products with powers of two, on values that are rounded already (exact).
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&t);
@@ -502,7 +504,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
         int64_t held = -1;
         int g = 0, p0 = 0, cnt = 0;
         int32_t rows[PIECES];  // the rows that this lane stores: quad rows lane / PIECES + (32 / PIECES) i
-        float rs = 1.f;        // 2^-k of this lane's row of the accumulator
+        uint32_t rs[PIECES];   // 2^-k of these rows, twice
         for (int64_t u = lo; u < hi; ++u) {
             const int64_t tile = u / ndc;
             const int d0 = (int)(u - tile * ndc) * ND;
@@ -513,8 +515,9 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                 for (int i = 0; i < PIECES; ++i) {
                     const int q = quad * 32 + lane / PIECES + 32 / PIECES * i;
                     rows[i] = q < cnt ? plan.perm[p0 + q] : -1;
+                    const __nv_bfloat162 two = __float2bfloat162_rn(q < cnt ? rinv[p0 + q] : 1.f);
+                    rs[i] = *reinterpret_cast<const uint32_t*>(&two);
                 }
-                if (quad * 32 + lane < cnt) rs = rinv[p0 + quad * 32 + lane];
             }
             if (cnt == 0) continue;
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sh->tfull[buf], bphase, abort_flag))) break;
@@ -538,7 +541,7 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                         uint32_t o[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(rs * __uint_as_float(v[8 * p + 2 * q]), rs * __uint_as_float(v[8 * p + 2 * q + 1]));
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[8 * p + 2 * q]), __uint_as_float(v[8 * p + 2 * q + 1]));
                             o[q] = *reinterpret_cast<const uint32_t*>(&b);
                         }
                         const int at = p ^ (lane & 7);
@@ -557,8 +560,9 @@ adapters_dx_tc_kernel(const __grid_constant__ CUtensorMap map_dh, const __grid_c
                         const int q = lane / PIECES + 32 / PIECES * i;
                         const int at = piece ^ (q & 7);
                         uint4 t = *reinterpret_cast<const uint4*>(mine + (q * PIECES + at) * 16);
-                        t = make_uint4(mul_bf16x2(t.x, cs[w / 64].x), mul_bf16x2(t.y, cs[w / 64].y), mul_bf16x2(t.z, cs[w / 64].z),
-                                       mul_bf16x2(t.w, cs[w / 64].w));
+                        const uint4 c = cs[w / 64];
+                        t = make_uint4(mul_bf16x2(mul_bf16x2(t.x, rs[i]), c.x), mul_bf16x2(mul_bf16x2(t.y, rs[i]), c.y),
+                                       mul_bf16x2(mul_bf16x2(t.z, rs[i]), c.z), mul_bf16x2(mul_bf16x2(t.w, rs[i]), c.w));
                         if (rows[i] >= 0 && col < d) *reinterpret_cast<uint4*>(dx + (int64_t)rows[i] * d + col) = t;
                     }
                 }
