@@ -82,7 +82,10 @@ __device__ __forceinline__ int fit_exponent(float top, int most) {
     frexpf(top, &e);  // top < 2^e
     return min(14 - e, most);
 }
-constexpr int kRowExponent = 100, kColExponent = 60;  // the most for rows of dh and of W_r
+// The most for rows of dh and of W_r: 2^126 is the last with a normal reciprocal; an adapter's column is scaled with its
+// row of W_r and may be far larger, so that stops where du A_a is still far from the end of fp32 (W_r's rows below 2^-60
+// lose bits).
+constexpr int kRowExponent = 126, kColExponent = 60;
 
 // v to within 2^-22 of itself (or 2^-25)
 __device__ __forceinline__ void split2h(float v, __half (&p)[2]) {
