@@ -128,13 +128,17 @@ __device__ __forceinline__ float row_softmax(float (&h)[4 * V]) {
 #pragma unroll
     for (int q = 0; q < 4 * V; ++q) { h[q] = expf(h[q] - top); s += h[q]; }
     s = lanes_sum<L>(s);
-    const float inv = s == 0.f ? 0.f : 1.f / s;
+    const float inv = s == 0.f ? 0.f : 1.f / (s == 0.f ? 1.f : s);
 #pragma unroll
     for (int q = 0; q < 4 * V; ++q) h[q] *= inv;
     return s == 0.f ? 0.f : top + logf(s);
 }
 
-__device__ __forceinline__ float logistic(float h) { return 1.f / (1.f + expf(-h)); }
+// By t = exp(-|h|), so that what is inverted lies in [1, 2]: the quotient of an infinity (the columns behind n) is slow.
+__device__ __forceinline__ float logistic(float h) {
+    const float t = expf(-fabsf(h)), w = 1.f / (1.f + t);
+    return h >= 0.f ? w : t * w;
+}
 
 template <int L, int V>
 __global__ void __launch_bounds__(rloss::kThreads, 4)
@@ -192,6 +196,11 @@ router_loss_chunk_kernel(const float* __restrict__ logits, const int32_t* __rest
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                if (!__any_sync(0xffffffffu, live[u])) {  // short sequences leave most of a round's rows empty
+#pragma unroll
+                    for (int q = 0; q < 4 * V; ++q) h[u][q] = 0.f;
+                    continue;
+                }
                 if (fn == MOE_SIGMOID) {
                     float e[4 * V];
 #pragma unroll
@@ -541,7 +550,7 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
             }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float inv = s[u] == 0.f ? 0.f : 1.f / s[u];
+            const float inv = s[u] == 0.f ? 0.f : 1.f / (s[u] == 0.f ? 1.f : s[u]);
             const float lse = s[u] == 0.f ? 0.f : top[u] + logf(s[u]);
             if (soft) {
                 const float c = eg[u] * inv - cz * lse;
@@ -552,7 +561,7 @@ router_loss_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
                 for (int q = 0; q < 4 * V; ++q) {  // rho (1 - rho) = t / (1 + t)^2, t = exp(-|h|): exact for large h
                     const float z = cz != 0.f ? cz * lse * inv * e[u][q] : 0.f;
                     const float t = expf(-fabsf(h[u][q])), s1 = 1.f + t, lost = t - (s1 - 1.f);  // 1 + t = s1 + lost
-                    e[u][q] = fmaf(g[u][q], t / fmaf(s1, s1, 2.f * s1 * lost), z);
+                    e[u][q] = fmaf(g[u][q], t * __frcp_rn(fmaf(s1, s1, 2.f * s1 * lost)), z);
                 }
             }
             if (chosen) {  // dL/dh of a pick: q_r (dg_r - sum q dg)
