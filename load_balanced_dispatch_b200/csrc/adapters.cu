@@ -604,6 +604,7 @@ rows_outer_kernel(RowsTasks tasks, int64_t m, int groups, AdapterPlan plan) {
             const int mid = (lo + hi) >> 1;
             if (plan.goff[mid] / T.seg + mid <= seg) lo = mid; else hi = mid;
         }
+        if (lo == groups - 1) return;  // rows without an adapter: nobody reads their sums
         const int64_t w = seg - lo;
         b = max(w * T.seg, (int64_t)plan.goff[lo]);
         end = min((w + 1) * T.seg, (int64_t)plan.goff[lo + 1]);
