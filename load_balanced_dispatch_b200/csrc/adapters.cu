@@ -74,7 +74,7 @@ struct PrepExtra {
 };
 
 // k such that values of magnitude up to `top` are below 2^14 after a product with 2^k (top 0, inf or NaN: 0), at most
-// `most`. Two fp16 parts then hold such a value to 2^-22 of itself or 2^-39 of the largest, and a product of two of
+// `most`. Two fp16 parts then hold such a value to 2^-22 of itself or 2^-38 of the largest, and a product of two of
 // them, or the sum of 256, is far from the ends of fp32.
 __device__ __forceinline__ int fit_exponent(float top, int most) {
     if (!(top > 0.f) || isinf(top)) return 0;

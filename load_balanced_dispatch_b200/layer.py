@@ -225,16 +225,17 @@ class MoELayer:
                                       (scale, f32, (na,), "scale"), (adapter_idx, torch.int32, (s.m,), "adapter_idx")):
             _chk(on, t, dtype, shape, name)
         self.disable_adapters()
-        self.adapters = dict(a=a, b=b, scale=scale, adapter_idx=adapter_idx, backward=backward, ran=False,
-                             split_combine=backward and self.ffn_combine)
-        self.buf["logits"] = torch.empty((s.m, s.n), dtype=f32, device=dev)
+        split = backward and self.ffn_combine
+        buf = dict(logits=torch.empty((s.m, s.n), dtype=f32, device=dev))
         if backward:
-            self.buf["hidden"] = torch.empty((s.m, r), dtype=f32, device=dev)
-        if self.adapters["split_combine"]:
-            self.ffn_combine = False
-            self.buf["ybuf"] = torch.empty((self.rows_max, s.d), dtype=s.dtype, device=dev)
+            buf["hidden"] = torch.empty((s.m, r), dtype=f32, device=dev)
+        if split:
+            buf["ybuf"] = torch.empty((self.rows_max, s.d), dtype=s.dtype, device=dev)
         size = moe_router_adapters_workspace_size(s.m, s.d, s.n, r, na, s.dtype)
         self.ws["adapters"] = torch.empty((max(size, 1),), dtype=u8, device=dev)
+        self.buf.update(buf)
+        self.ffn_combine = self.ffn_combine and not split
+        self.adapters = dict(a=a, b=b, scale=scale, adapter_idx=adapter_idx, backward=backward, ran=False, split_combine=split)
 
     def disable_adapters(self) -> None:
         """Back to the layer without adapters. As enable_adapters, it waits for the device and drops the captured

@@ -652,7 +652,7 @@ def test_adapters_backward_dx_at_any_scale(m, d, n, r, na):
         rows = (i["adapter_idx"] == q).nonzero()[:, 0]
         ref[rows] += s[q] * dh64[rows] @ b[q] @ a[q]
         mag[rows] += s[q] * dh64[rows].abs() @ b[q].abs() @ a[q].abs()
-    # as above, 2^-39 of the largest product of the row's and the column's values for each of n terms, and half a step of
+    # as above, 2^-38 of the largest product of the row's and the column's values for each of n terms, and half a step of
     # bf16's subnormal values
     top = 2.0 ** -134 + n * 2.0 ** -38 * dh64.abs().amax(1)[:, None] * w.abs().amax(1)
     within(dx, ref, 2.0 ** -8 * ref.abs() + (12 * -(-n // 64) + 12 + n + 6) * EPS * mag + top, "dx")

@@ -82,6 +82,23 @@ def test_enable_adapters_refuses_and_changes_nothing(monkeypatch, key, bad):
     assert layer.adapters is before and layer.buf == buf and layer.graph_all == "captured"
 
 
+def test_enable_adapters_without_memory_leaves_the_plain_layer(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda dev: None)
+    layer = bare_layer(k=1)
+    layer.disable_adapters()
+    layer.ffn_combine, layer.rows_max = True, 64
+    empty = torch.empty
+
+    def short(shape, **kw):
+        if tuple(shape) == (64, 32):  # the expert rows
+            raise torch.cuda.OutOfMemoryError("out of memory")
+        return empty(shape, **kw)
+    monkeypatch.setattr(torch, "empty", short)
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        layer.enable_adapters(**some_adapters(layer))
+    assert layer.adapters is None and layer.ffn_combine and "logits" not in layer.buf
+
+
 def test_router_backward_needs_a_forward_with_these_adapters(monkeypatch, calls):
     monkeypatch.setattr(torch.cuda, "synchronize", lambda dev: None)
     layer = bare_layer()
