@@ -6,6 +6,12 @@ import torch
 from load_balanced_dispatch_b200 import layer as L
 
 
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from load_balanced_dispatch_b200 import build
+    build.build()
+
+
 @pytest.fixture
 def calls(monkeypatch):
     """Stands in for the entry points that router_backward calls; the list of (name, keyword arguments)."""
